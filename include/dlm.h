@@ -368,6 +368,119 @@ int dlm_attention_noalloc(const void *q, const void *k_cache, const void *v_cach
  * word is shared by every caller on the device. */
 int dlm_attention_noalloc_check(void *stream);
 
+/* ---- paged KV cache --------------------------------------------------------
+ * Pages of `page_size` token slots that sequences of any length share, for
+ * batches whose lengths differ and change (course "Diffusion LLMs", section
+ * 14: the finished prefix is cached and grows block by block; DiffusionGemma
+ * page: several canvases in one batch).  The calls take no context: the
+ * caller owns the cache, the tables, the free list and the workspace, and
+ * lengths live on the device, so that a whole step (resize, write, attend)
+ * can be captured into one CUDA graph whatever the lengths turn out to be.
+ *
+ *   block table  int32 [batch][table_width]: entry j of row b is the page
+ *                that holds positions j*page_size .. of sequence b; entries
+ *                past ceil(length / page_size) are never read.
+ *   slot         page * page_size + offset in the page, int64.
+ *   free list    a stack: free_pages[0 .. n_free) are the unused page ids.
+ *
+ * All pointers are device pointers of the current device, and `stream`
+ * belongs to it; DLM_EINVAL otherwise.  Errors found on the device (a page id
+ * outside the cache, lengths or offsets out of range, a bounded wait that ran
+ * out) are recorded in a word of the device that dlm_paged_check reads; the
+ * access is skipped. */
+
+/* A cache: k and v are [n_pages][n_kv_heads][page_size][head_dim], 16-byte
+ * aligned.  page_size: 8, 16, 32, 64, 128 or 256.  dtype DLM_BF16 (head_dim
+ * 64 or 128) or DLM_F32 (head_dim 32, 64 or 128).  Slots that no write has
+ * filled may hold anything. */
+typedef struct {
+  void *k, *v;
+  int n_pages, page_size, n_kv_heads, head_dim, dtype;
+} dlm_paged_cache;
+
+/* Grow and shrink sequences: block tables, the free list and the slot map of
+ * the new tokens from request lengths, in one launch.  Sequence b goes from
+ * cur_lens[b] to new_lens[b] tokens (int32 [batch], batch <= 4096).
+ *   - Shrinking releases the pages past ceil(new / page_size); a new length
+ *     of 0 ends the sequence.
+ *   - Growing takes pages and writes their ids into the table.  Requests are
+ *     served in order: a sequence that needs pages is refused when it and
+ *     the sequences before it need more than the free list and the released
+ *     pages hold, and any that grows when the new tokens up to and including
+ *     its own exceed max_new.  A length below 0 or beyond table_width pages
+ *     is refused as well.
+ *   out_lens [batch]  new_lens where served, cur_lens where refused
+ *   cu_new [batch+1]  offsets of the sequences' new tokens, max(0, new -
+ *            cur) each, refused ones included (so that the rows of the
+ *            others do not move); capped at max_new
+ *   slots [max_new]   slot of every new token in that order; -1 for a
+ *            refused sequence's and behind the last one.  NULL if max_new
+ *            is 0.
+ *   n_free_in, n_free_out  the stack's height before and after.
+ * out_lens may be cur_lens or new_lens, and n_free_out may be n_free_in.
+ * Order of the stack: the released pages are pushed so that the first
+ * (lowest sequence, lowest table column) is on top, then the new pages are
+ * popped in order; growing and then shrinking back restores the stack.
+ * A stack height outside [0, n_pages], or releases that would pass n_pages,
+ * change nothing but the error word (out_lens = cur_lens, slots -1). */
+int dlm_paged_resize(const int32_t *cur_lens, const int32_t *new_lens, int32_t *out_lens,
+                     int batch, int32_t *block_table, int table_width, int page_size,
+                     int32_t *free_pages, int n_pages, const int32_t *n_free_in,
+                     int32_t *n_free_out, int32_t *cu_new, int64_t *slots, int max_new,
+                     void *stream);
+
+/* Write n_tokens rows of K and V into the cache: row t ([n_kv_heads]
+ * [head_dim], rows k_stride / v_stride elements apart, already rotated, in
+ * the cache's type) goes to slots[t].  A negative slot is skipped (padding).
+ * Two rows with the same slot leave one of the two (which one is not
+ * defined).  k and v are 16-byte aligned and the strides multiples of 16
+ * bytes and at least n_kv_heads * head_dim; k and v do not overlap the
+ * cache. */
+int dlm_paged_kv_write(const dlm_paged_cache *cache, const void *k, const void *v,
+                       int64_t k_stride, int64_t v_stride, const int64_t *slots, int n_tokens,
+                       void *stream);
+
+/* Bytes of workspace that dlm_paged_attention needs for this cache and
+ * n_heads query heads on the current device: the partial results of query
+ * tiles whose keys are split over SMs.  It does not depend on lengths or the
+ * batch.  Nothing is kept in it between calls, but calls that may run at the
+ * same time (two streams, two captured graphs) need one each. */
+int dlm_paged_attention_workspace(const dlm_paged_cache *cache, int n_heads, size_t *bytes);
+
+/* Attention of ragged chunks of new tokens over a paged cache that already
+ * holds them (dlm_paged_kv_write first).
+ *   q        [n_tokens][n_heads][head_dim], rows q_stride elements apart, in
+ *            the cache's type; sequence b's rows are cu_q[b] .. cu_q[b+1] - 1
+ *   cu_q     int32 [batch+1], ascending from >= 0 to <= n_tokens
+ *   ctx_lens int32 [batch]: length of sequence b, its chunk included: row i of
+ *            a chunk of n is position ctx - n + i
+ *   mask_block  0: every row sees all of [0, ctx) (a canvas being denoised);
+ *            1: causal; c > 1: causal between blocks of c positions (the
+ *            clean pass over finished blocks): the row at position p sees
+ *            keys below min(ctx, (p / c + 1) * c)
+ *   scale    of the scores; 0 means 1 / sqrt(head_dim)
+ *   o        [n_tokens][n_heads][head_dim], rows o_stride elements apart
+ *   lse      float32 [n_tokens][n_heads], or NULL: log of the sum of the
+ *            exponentials of the scaled scores
+ * A row that sees no key (ctx 0, or mask_block >= 1 and a position below 0)
+ * gets zeros and lse -inf; rows of o and lse outside [cu_q[0],
+ * cu_q[batch]) are left as they were.  Keys that a row does not see do not reach its
+ * result, whatever their K and V hold (infinities and NaN included).
+ * n_heads is a multiple of n_kv_heads, at most 128 query heads per KV head;
+ * batch <= 4096.  q and o are 16-byte aligned, their strides multiples of 16
+ * bytes and at least n_heads * head_dim; o does not overlap q, the cache or
+ * the workspace.  `workspace` is 256-byte aligned. */
+int dlm_paged_attention(const dlm_paged_cache *cache, const void *q, int64_t q_stride, void *o,
+                        int64_t o_stride, float *lse, const int32_t *cu_q,
+                        const int32_t *ctx_lens, const int32_t *block_table, int table_width,
+                        int batch, int n_tokens, int n_heads, int mask_block, float scale,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* Synchronise `stream`, then read and clear the current device's error word
+ * of the paged calls: DLM_OK, DLM_EBOUNDS or DLM_ETIMEOUT (the text is in
+ * dlm_last_error(NULL)). */
+int dlm_paged_check(void *stream);
+
 /* Synchronise `stream` and return the device error word (DLM_OK, or
  * DLM_ETIMEOUT / DLM_EBOUNDS set by a kernel); clears it. */
 int dlm_check(dlm_ctx *ctx, void *stream);

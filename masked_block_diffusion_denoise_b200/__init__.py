@@ -29,6 +29,8 @@ __all__ = [
     "DLM_NUM_STAGES", "dlm_attention_noalloc", "dlm_attention_noalloc_check",
     "dlm_trace_layout", "dlm_trace_read", "dlm_trace_clear", "dlm_decode_steps",
     "dlm_attention_plan", "dlm_test_withhold_loads", "dlm_test_exp2",
+    "dlm_paged_cache", "dlm_paged_resize", "dlm_paged_kv_write", "dlm_paged_attention_workspace",
+    "dlm_paged_attention", "dlm_paged_check",
 ]
 
 DLM_OK, DLM_EINVAL, DLM_ENOMEM, DLM_ECUDA, DLM_ECAP, DLM_ETIMEOUT, DLM_EBOUNDS, DLM_ESTATE = \
@@ -85,6 +87,14 @@ class dlm_canvas_stats(ctypes.Structure):
                 ("frozen", ctypes.c_int32), ("edited", ctypes.c_int32)]
 
 
+class dlm_paged_cache(ctypes.Structure):
+    """A paged KV cache: (k address, v address, n_pages, page_size,
+    n_kv_heads, head_dim, dtype); see include/dlm.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
 class DlmError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__("dlm error %d: %s" % (code, msg))
@@ -93,6 +103,8 @@ class DlmError(RuntimeError):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+_Z = ctypes.c_size_t
 _SIGS = {
     "dlm_create": (_I, [ctypes.POINTER(dlm_model_desc), ctypes.POINTER(dlm_weights),
                         ctypes.POINTER(_P)]),
@@ -121,6 +133,13 @@ _SIGS = {
     "dlm_set_stage_events": (_I, [_P, _I, ctypes.POINTER(_P), _I]),
     "dlm_attention_noalloc": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "dlm_attention_noalloc_check": (_I, [_P]),
+    "dlm_paged_resize": (_I, [_P, _P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _P]),
+    "dlm_paged_kv_write": (_I, [ctypes.POINTER(dlm_paged_cache), _P, _P, _L, _L, _P, _I, _P]),
+    "dlm_paged_attention_workspace": (_I, [ctypes.POINTER(dlm_paged_cache), _I,
+                                           ctypes.POINTER(_Z)]),
+    "dlm_paged_attention": (_I, [ctypes.POINTER(dlm_paged_cache), _P, _L, _P, _L, _P, _P, _P, _P,
+                                 _I, _I, _I, _I, _I, ctypes.c_float, _P, _Z, _P]),
+    "dlm_paged_check": (_I, [_P]),
     "dlm_check": (_I, [_P, _P]),
     "dlm_launches_per_step": (_I, [_P]),
     "dlm_test_withhold_loads": (_I, [_P, _I]),
@@ -305,6 +324,55 @@ def dlm_attention_noalloc_check(stream=None) -> int:
     if rc != DLM_OK:
         raise DlmError(rc, lib().dlm_last_error(None).decode())
     return rc
+
+
+def dlm_paged_resize(cur_lens, new_lens, out_lens, batch: int, block_table, table_width: int,
+                     page_size: int, free_pages, n_pages: int, n_free_in, n_free_out, cu_new,
+                     slots, max_new: int, stream=None) -> int:
+    """Grow and shrink sequences' pages; slot map of the new tokens."""
+    return _check(None, lib().dlm_paged_resize(
+        _ptr(cur_lens), _ptr(new_lens), _ptr(out_lens), batch, _ptr(block_table), table_width,
+        page_size, _ptr(free_pages), n_pages, _ptr(n_free_in), _ptr(n_free_out), _ptr(cu_new),
+        _ptr(slots), max_new, _stream(stream)))
+
+
+def dlm_paged_kv_write(cache: dlm_paged_cache, k, v, slots, n_tokens: int, k_stride: int = 0,
+                       v_stride: int = 0, stream=None) -> int:
+    """Rows of K and V into the cache's slots; a stride of 0 means rows
+    without gaps (n_kv_heads * head_dim elements)."""
+    row = cache.n_kv_heads * cache.head_dim
+    return _check(None, lib().dlm_paged_kv_write(ctypes.byref(cache), _ptr(k), _ptr(v),
+                                                 k_stride or row, v_stride or row, _ptr(slots),
+                                                 n_tokens, _stream(stream)))
+
+
+def dlm_paged_attention_workspace(cache: dlm_paged_cache, n_heads: int) -> int:
+    """Bytes of workspace dlm_paged_attention needs on the current device."""
+    n = _Z()
+    _check(None, lib().dlm_paged_attention_workspace(ctypes.byref(cache), n_heads,
+                                                     ctypes.byref(n)))
+    return n.value
+
+
+def dlm_paged_attention(cache: dlm_paged_cache, q, o, cu_q, ctx_lens, block_table,
+                        table_width: int, batch: int, n_tokens: int, n_heads: int,
+                        mask_block: int, workspace, lse=None, scale: float = 0.0,
+                        q_stride: int = 0, o_stride: int = 0, stream=None) -> int:
+    """Attention of ragged chunks over a paged cache; `workspace` is a device
+    tensor of dlm_paged_attention_workspace bytes, a stride of 0 means rows
+    without gaps (n_heads * head_dim elements)."""
+    row = n_heads * cache.head_dim
+    return _check(None, lib().dlm_paged_attention(
+        ctypes.byref(cache), _ptr(q), q_stride or row, _ptr(o), o_stride or row, _ptr(lse),
+        _ptr(cu_q), _ptr(ctx_lens), _ptr(block_table), table_width, batch, n_tokens, n_heads,
+        mask_block, scale, _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
+def dlm_paged_check(stream=None) -> int:
+    """Read and clear the device error word of the paged calls; raises
+    DlmError(DLM_EBOUNDS / DLM_ETIMEOUT) when a kernel recorded one."""
+    return _check(None, lib().dlm_paged_check(_stream(stream)))
 
 
 def dlm_check(ctx, stream=None) -> int:

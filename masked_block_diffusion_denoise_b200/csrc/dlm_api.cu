@@ -192,6 +192,18 @@ bool map_q(CUtensorMap* m, void* q, uint64_t positions, uint64_t H, uint64_t Dh,
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+}  // namespace
+
+// for the entry points of other files that take no context
+namespace dlm {
+int api_fail(int code, const char* what) { return fail(nullptr, code, what); }
+int api_cuda_fail(const char* where, cudaError_t e) { return cuda_fail(nullptr, where, e); }
+void api_clear_error() { g_create_error.clear(); }
+void* api_encode_tiled() { return reinterpret_cast<void*>(encode_fn()); }
+}  // namespace dlm
+
+namespace {
+
 // ---------------------------------------------------------------------------
 // work plans
 // ---------------------------------------------------------------------------

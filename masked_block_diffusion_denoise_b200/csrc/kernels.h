@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "lm_epilogue.cuh"
 
 namespace dlm {
@@ -202,5 +204,77 @@ cudaError_t commit_step(const SelectArgs& a, int32_t* tokens, uint8_t* committed
                         uint8_t* done, int32_t* eos_pos, int32_t* prev_cand, int32_t* stable,
                         const float* part, int n_part, int32_t* cand, float* conf, float* ent,
                         dlm_canvas_stats* stats, const int* n_active, int* err, cudaStream_t st);
+
+// A result computed once per device (function attributes are per device)
+constexpr int kMaxDeviceOnce = 64;
+struct DeviceOnce {
+  std::once_flag flag[kMaxDeviceOnce];
+  cudaError_t result[kMaxDeviceOnce];
+  template <typename F>
+  cudaError_t get(F&& f) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDeviceOnce) return cudaErrorInvalidDevice;
+    std::call_once(flag[dev], [&] { result[dev] = f(); });
+    return result[dev];
+  }
+};
+
+// ---- paged.cu: the paged KV cache ---------------------------------------------
+constexpr int kPagedMaxBatch = 4096;   // sequences of a paged call (their scan state is in shared memory)
+
+// block tables, free list and slot map from request lengths (see dlm.h)
+struct PagedResize {
+  const int32_t* cur;
+  const int32_t* want;
+  int32_t* out_lens;
+  int B;
+  int32_t* table;
+  int W;
+  int page_shift;
+  int32_t* free_pages;
+  int n_pages;
+  const int32_t* n_free_in;
+  int32_t* n_free_out;
+  int32_t* cu;
+  int64_t* slots;
+  int max_new;
+  int* err;
+};
+cudaError_t paged_resize(const PagedResize& a, cudaStream_t st);
+
+// the cache of a paged call: pages [n_pages][Hkv][1 << page_shift][Dh]
+struct PagedKV {
+  void* k;
+  void* v;
+  int n_pages, page_shift, Hkv, Dh, esize;
+};
+cudaError_t paged_kv_write(const PagedKV& c, const void* k, const void* v, int64_t k_stride,
+                           int64_t v_stride, const int64_t* slots, int n, int* err,
+                           cudaStream_t st);
+
+struct PagedAttn {
+  PagedKV c;
+  const void* q;
+  int64_t q_stride;        // elements between rows
+  void* o;
+  int64_t o_stride;
+  float* lse;              // [T][H] or null
+  const int32_t* cu;       // [B + 1]
+  const int32_t* ctx;      // [B]
+  const int32_t* table;    // [B][W]
+  int W, B, T, H;
+  int block;               // mask: 0 none, 1 causal, c block-causal
+  float scale;
+  void* work;
+  int* err;
+};
+cudaError_t paged_attention_simt(const PagedAttn& a, cudaStream_t st);
+
+// ---- dlm_api.cu: errors and driver entry points for context-free calls -----------
+int api_fail(int code, const char* what);
+int api_cuda_fail(const char* where, cudaError_t e);
+void api_clear_error();
+void* api_encode_tiled();   // cuTensorMapEncodeTiled, or null
 
 }  // namespace dlm

@@ -1,0 +1,349 @@
+// The paged KV cache: block tables, free list and slot map from request
+// lengths, and the write of new tokens' K and V into their slots.  (A finished
+// block joins the cache of its sequence: course "Diffusion LLMs", section 14.)
+#include <climits>
+
+#include <cooperative_groups.h>
+#include <math_constants.h>
+
+#include "kernels.h"
+
+namespace dlm {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+// ---------------------------------------------------------------------------
+// Resize.  With pages(n) = ceil(n / P), per sequence
+//   need = max(0, pages(new) - pages(cur)), gone = max(0, pages(cur) - pages(new)),
+//   tok = max(0, new - cur);
+// three exclusive prefix sums over the batch (D, F, T) say everything else:
+// the k-th new page of the batch is entry top-1-k of the stack, where the
+// stack is the free list with the released pages pushed in reverse order, so
+// k < F_total is released page k and the others come from the free list.
+// Every thread can therefore compute any output by itself, and no output is
+// read back: one launch, one cluster, no order of atomics.  Each CTA of the
+// cluster scans the batch for itself (its sequences' state in shared memory)
+// and then takes its share of the outputs; the cluster barrier between the
+// two allows the outputs to overwrite the inputs.
+// ---------------------------------------------------------------------------
+constexpr int kResizeThreads = 1024;
+constexpr int kResizeSeqs = kPagedMaxBatch;
+
+struct Scan3 {
+  long long need, gone, tok;
+};
+__device__ __forceinline__ Scan3 operator+(const Scan3& a, const Scan3& b) {
+  return Scan3{a.need + b.need, a.gone + b.gone, a.tok + b.tok};
+}
+__device__ __forceinline__ Scan3 shfl_up3(const Scan3& a, int d) {
+  return Scan3{__shfl_up_sync(0xffffffffu, a.need, d), __shfl_up_sync(0xffffffffu, a.gone, d),
+               __shfl_up_sync(0xffffffffu, a.tok, d)};
+}
+
+// largest i in [0, n) with first[i] <= x, for ascending first, first[0] <= x
+__device__ __forceinline__ int find_last(const int* first, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedResize a) {
+  extern __shared__ int sm[];
+  int* s_cur = sm;               // [B] length now
+  int* s_new = s_cur + a.B;      // [B] length wanted
+  int* s_need = s_new + a.B;     // [B] D: new pages before this sequence's
+  int* s_gone = s_need + a.B;    // [B] F: released pages before this sequence's
+  int* s_tok = s_gone + a.B;     // [B] T: new tokens before this sequence's, capped at max_new
+  int* s_ok = s_tok + a.B;       // [B] served
+  __shared__ Scan3 warp_sum[32];
+  __shared__ long long s_total[3];   // pages taken, pages released, tokens
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x, n_ranks = gridDim.x;
+  const int sh = a.page_shift;
+  const long long page_mask = (1ll << sh) - 1;
+  const int n_free = *a.n_free_in;
+  auto pages = [&](int n) { return (int)(((long long)n + page_mask) >> sh); };
+
+  // this thread's consecutive sequences
+  const int per = (a.B + kResizeThreads - 1) / kResizeThreads;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  auto change = [&](int cur, int want) {
+    Scan3 c{0, 0, 0};
+    if (cur < 0 || want < 0) return c;
+    const int pc = pages(cur), pn = pages(want);
+    if (pn <= a.W && pc <= a.W) {
+      c.need = max(0, pn - pc);
+      c.gone = max(0, pc - pn);
+    }
+    c.tok = max(0, want - cur);
+    return c;
+  };
+  Scan3 mine{0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    const int cur = a.cur[b], want = a.want[b];
+    s_cur[b] = cur;
+    s_new[b] = want;
+    mine = mine + change(cur, want);
+  }
+  Scan3 incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Scan3 o = shfl_up3(incl, d);
+    if (lane >= d) incl = incl + o;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  if (tid < 3) s_total[tid] = 0;
+  __syncthreads();
+  Scan3 before{0, 0, 0}, all{0, 0, 0};
+  for (int w = 0; w < kResizeThreads / 32; ++w) {
+    if (w == warp) before = all;
+    all = all + warp_sum[w];
+  }
+  Scan3 at = Scan3{before.need + incl.need - mine.need, before.gone + incl.gone - mine.gone,
+                   before.tok + incl.tok - mine.tok};
+  // a broken stack: nothing changes
+  const bool broken = n_free < 0 || n_free > a.n_pages || n_free + all.gone > a.n_pages;
+  const long long have = broken ? 0 : n_free + all.gone;
+  long long taken = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int cur = s_cur[b], want = s_new[b];
+    const Scan3 c = change(cur, want);
+    const bool fits = cur >= 0 && want >= 0 && pages(want) <= a.W && pages(cur) <= a.W;
+    const bool ok = !broken && fits && (c.need == 0 || at.need + c.need <= have) &&
+                    (c.tok == 0 || at.tok + c.tok <= a.max_new);
+    s_ok[b] = ok;
+    s_need[b] = (int)min(at.need, (long long)INT_MAX);
+    s_gone[b] = (int)min(at.gone, (long long)INT_MAX);
+    s_tok[b] = (int)min(at.tok, (long long)a.max_new);
+    if (ok) taken += c.need;
+    at = at + c;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) taken += __shfl_xor_sync(0xffffffffu, taken, d);
+  // whole numbers: the order of the additions does not matter
+  if (lane == 0 && taken > 0)
+    atomicAdd(reinterpret_cast<unsigned long long*>(&s_total[0]), (unsigned long long)taken);
+  __syncthreads();
+  // every CTA has read the lengths and the stack's height
+  if (n_ranks > 1) cg::this_cluster().sync();
+
+  const int F = broken ? 0 : (int)all.gone;
+  const int K = (int)s_total[0];
+  const int n_tok = (int)min(all.tok, (long long)a.max_new);
+  // page id j of the released ones, and the k-th popped one
+  auto checked = [&](int page) {
+    if (page < 0 || page >= a.n_pages) raise_error(a.err, DLM_EBOUNDS);
+    return page;
+  };
+  auto released = [&](int j) {
+    const int b = find_last(s_gone, a.B, j);
+    return checked(a.table[(size_t)b * a.W + pages(s_new[b]) + (j - s_gone[b])]);
+  };
+  auto popped = [&](int k) {
+    return k < F ? released(k) : checked(a.free_pages[n_free + F - 1 - k]);
+  };
+  const int first = rank * kResizeThreads + tid, step = n_ranks * kResizeThreads;
+  if (first == 0) {
+    if (broken) raise_error(a.err, DLM_EBOUNDS);
+    *a.n_free_out = broken ? n_free : n_free + F - K;
+    a.cu[0] = 0;
+  }
+  for (int b = first; b < a.B; b += step) {
+    a.out_lens[b] = s_ok[b] ? s_new[b] : s_cur[b];
+    a.cu[b + 1] = b + 1 < a.B ? s_tok[b + 1] : n_tok;
+  }
+  // new pages into the tables (served sequences that need pages are the
+  // first of those that need any, so page k's owner is found in D)
+  for (int k = first; k < K; k += step) {
+    const int b = find_last(s_need, a.B, k);
+    a.table[(size_t)b * a.W + pages(s_cur[b]) + (k - s_need[b])] = popped(k);
+  }
+  // released pages that stay on the stack
+  for (int pos = n_free + first; pos < n_free + F - K; pos += step)
+    a.free_pages[pos] = released(F - 1 - (pos - n_free));
+  // a slot per new token
+  for (int t = first; t < a.max_new; t += step) {
+    int64_t slot = -1;
+    if (t < n_tok) {
+      const int b = find_last(s_tok, a.B, t);
+      if (s_ok[b]) {
+        const int cur = s_cur[b];
+        const int pos = cur + (t - s_tok[b]);
+        const int col = pos >> sh, pc = pages(cur);
+        const int page = col < pc ? checked(a.table[(size_t)b * a.W + col])
+                                  : popped(s_need[b] + (col - pc));
+        if (page >= 0 && page < a.n_pages) slot = ((int64_t)page << sh) + (pos & (int)page_mask);
+      }
+    }
+    a.slots[t] = slot;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// K/V rows into their slots: a copy in 16-byte pieces.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) kv_write_kernel(const PagedKV c, const uint8_t* __restrict__ k,
+                                                       const uint8_t* __restrict__ v,
+                                                       int64_t k_stride, int64_t v_stride,
+                                                       const int64_t* __restrict__ slots, int n,
+                                                       int* err) {
+  const int head_chunks = c.Dh * c.esize / 16;
+  const int row_chunks = c.Hkv * head_chunks;
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (int64_t)n * row_chunks) return;
+  const int t = (int)(i / row_chunks), j = (int)(i % row_chunks);
+  const int64_t slot = slots[t];
+  if (slot < 0) return;
+  const int64_t page = slot >> c.page_shift;
+  if (page >= c.n_pages) {
+    raise_error(err, DLM_EBOUNDS);
+    return;
+  }
+  const int off = (int)(slot & ((1 << c.page_shift) - 1));
+  const int head = j / head_chunks, part = j % head_chunks;
+  const size_t dst = ((((size_t)page * c.Hkv + head) << c.page_shift) + off) * head_chunks + part;
+  reinterpret_cast<uint4*>(c.k)[dst] = *reinterpret_cast<const uint4*>(k + t * k_stride + j * 16);
+  reinterpret_cast<uint4*>(c.v)[dst] = *reinterpret_cast<const uint4*>(v + t * v_stride + j * 16);
+}
+
+// ---------------------------------------------------------------------------
+// Attention, one warp per (query row, head): online softmax over the visible
+// keys, Dh / 32 dimensions a lane.
+// ---------------------------------------------------------------------------
+// offsets ascending within the rows, a length that the table can hold
+__device__ __forceinline__ bool sequence_ok(const PagedAttn& a, int b) {
+  const int c0 = a.cu[b], c1 = a.cu[b + 1], ctx = a.ctx[b];
+  return c0 >= 0 && c0 <= c1 && c1 <= a.T && ctx >= 0 &&
+         (long long)ctx <= ((long long)a.W << a.c.page_shift);
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(128) attend_kernel(const PagedAttn a) {
+  constexpr int E = DH / 32;
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x)
+      if (!sequence_ok(a, b)) raise_error(a.err, DLM_EBOUNDS);
+  const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (wid >= (int64_t)a.T * a.H) return;
+  const int t = (int)(wid / a.H), h = (int)(wid % a.H);
+  // the sequence of this row
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int b = lo;
+  const int n = a.cu[b + 1] - a.cu[b], i = t - a.cu[b], ctx = a.ctx[b];
+  const int P = 1 << a.c.page_shift;
+  if (i < 0 || i >= n || !sequence_ok(a, b)) return;
+  const int pos = ctx - n + i;
+  int limit = ctx;
+  if (a.block > 0) limit = pos < 0 ? 0 : (int)min((long long)ctx, ((long long)pos / a.block + 1) * a.block);
+  const int g = h / (a.H / a.c.Hkv);
+  const T* q = reinterpret_cast<const T*>(a.q) + t * a.q_stride + h * DH;
+  float qr[E], acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    qr[e] = to_f32(q[e * 32 + lane]) * a.scale;
+    acc[e] = 0.f;
+  }
+  float m = -CUDART_INF_F, l = 0.f;
+  for (int j = 0; j < limit; ++j) {
+    const int page = a.table[(size_t)b * a.W + (j >> a.c.page_shift)];
+    if (page < 0 || page >= a.c.n_pages) {
+      if (lane == 0) raise_error(a.err, DLM_EBOUNDS);
+      continue;
+    }
+    const size_t row = (((size_t)page * a.c.Hkv + g) << a.c.page_shift) + (j & (P - 1));
+    const T* kp = reinterpret_cast<const T*>(a.c.k) + row * DH;
+    const T* vp = reinterpret_cast<const T*>(a.c.v) + row * DH;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(qr[e], to_f32(kp[e * 32 + lane]), s);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    const float m_new = fmaxf(m, s);
+    const float base = m_new == -CUDART_INF_F ? 0.f : m_new;
+    const float alpha = expf(m - base), p = expf(s - base);
+    l = l * alpha + p;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * alpha + p * to_f32(vp[e * 32 + lane]);
+    m = m_new;
+  }
+  T* o = reinterpret_cast<T*>(a.o) + t * a.o_stride + h * DH;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e * 32 + lane] = from_f32<T>(acc[e] * inv);
+  if (a.lse != nullptr && lane == 0) a.lse[(size_t)t * a.H + h] = l == 0.f ? -CUDART_INF_F : m + logf(l);
+}
+
+}  // namespace
+
+cudaError_t paged_resize(const PagedResize& a, cudaStream_t st) {
+  const int smem = 6 * a.B * (int)sizeof(int);
+  static_assert(6 * kResizeSeqs * sizeof(int) <= 227 * 1024 - 2048, "batch exceeds shared memory");
+  static DeviceOnce once;
+  cudaError_t e = once.get([] {
+    return cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                6 * kResizeSeqs * (int)sizeof(int));
+  });
+  if (e != cudaSuccess) return e;
+  // one CTA up to two outputs a thread, then a cluster of up to 8
+  int ranks = 1;
+  while (ranks < 8 && (long long)ranks * 2 * kResizeThreads < a.max_new) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(kResizeThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ranks;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, resize_kernel, a);
+}
+
+cudaError_t paged_kv_write(const PagedKV& c, const void* k, const void* v, int64_t k_stride,
+                           int64_t v_stride, const int64_t* slots, int n, int* err,
+                           cudaStream_t st) {
+  const int64_t pieces = (int64_t)n * c.Hkv * (c.Dh * c.esize / 16);
+  kv_write_kernel<<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(
+      c, (const uint8_t*)k, (const uint8_t*)v, k_stride * c.esize, v_stride * c.esize, slots, n,
+      err);
+  return cudaGetLastError();
+}
+
+cudaError_t paged_attention_simt(const PagedAttn& a, cudaStream_t st) {
+  const int64_t warps = (int64_t)a.T * a.H;
+  const unsigned grid = (unsigned)((warps + 3) / 4);
+  const bool bf = a.c.esize == 2;
+  if (bf && a.c.Dh == 64)
+    attend_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(a);
+  else if (bf)
+    attend_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(a);
+  else if (a.c.Dh == 32)
+    attend_kernel<float, 32><<<grid, 128, 0, st>>>(a);
+  else if (a.c.Dh == 64)
+    attend_kernel<float, 64><<<grid, 128, 0, st>>>(a);
+  else
+    attend_kernel<float, 128><<<grid, 128, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace dlm
