@@ -269,7 +269,11 @@ struct PagedAttn {
   void* work;
   int* err;
 };
-cudaError_t paged_attention_simt(const PagedAttn& a, cudaStream_t st);
+cudaError_t paged_attention_simt(const PagedAttn& a, cudaStream_t st);   // any type
+
+// ---- paged_attention.cu: bf16 on the tensor cores ---------------------------------
+size_t paged_attention_work(int Dh, int num_sms);   // bytes of workspace
+cudaError_t paged_attention_tc(const PagedAttn& a, int num_sms, cudaStream_t st);
 
 // ---- dlm_api.cu: errors and driver entry points for context-free calls -----------
 int api_fail(int code, const char* what);

@@ -16,12 +16,13 @@ struct PagedDevice {
   std::once_flag once;
   cudaError_t status = cudaErrorNotReady;
   int* err = nullptr;
+  int num_sms = 0;
 };
 constexpr int kMaxDevices = 64;
 PagedDevice g_paged[kMaxDevices];
 
 // the current device's state in *out, looked up on first use; a DLM status
-int paged_device(PagedDevice** out, int* device) {
+int paged_device(PagedDevice** out, int* device = nullptr) {
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) {
     cudaGetLastError();
@@ -29,14 +30,16 @@ int paged_device(PagedDevice** out, int* device) {
   }
   if (dev < 0 || dev >= kMaxDevices) return api_fail(DLM_EINVAL, "paged: device index out of range");
   PagedDevice& d = g_paged[dev];
-  std::call_once(d.once, [&d] {
+  std::call_once(d.once, [&d, dev] {
     void* p = nullptr;
     d.status = cudaGetSymbolAddress(&p, g_paged_err);
     d.err = static_cast<int*>(p);
+    if (d.status == cudaSuccess)
+      d.status = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
   });
-  if (d.status != cudaSuccess) return api_cuda_fail("paged: cudaGetSymbolAddress", d.status);
+  if (d.status != cudaSuccess) return api_cuda_fail("paged: device set-up", d.status);
   *out = &d;
-  *device = dev;
+  if (device != nullptr) *device = dev;
   return DLM_OK;
 }
 
@@ -69,8 +72,14 @@ const char* cache_problem(const dlm_paged_cache* c) {
     return "paged: head_dim must be 64 or 128 (32 too for DLM_F32)";
   if (page_shift(c->page_size) < 0) return "paged: page_size must be 8, 16, 32, 64, 128 or 256";
   if (c->n_kv_heads < 1 || c->n_pages < 1) return "paged: need n_kv_heads and n_pages >= 1";
-  if (c->n_kv_heads > 65536 || (long long)c->n_pages * c->n_kv_heads > INT_MAX)
-    return "paged: n_pages * n_kv_heads exceeds 2^31 - 1";
+  if (c->n_kv_heads > 65536 || ((long long)c->n_pages + 1) * c->n_kv_heads > INT_MAX)
+    return "paged: (n_pages + 1) * n_kv_heads exceeds 2^31 - 1";
+  return nullptr;
+}
+
+const char* heads_problem(const dlm_paged_cache* c, int n_heads) {
+  if (n_heads < 1 || n_heads % c->n_kv_heads != 0 || n_heads / c->n_kv_heads > 128)
+    return "paged_attention: n_heads must be a multiple of n_kv_heads, at most 128 times it";
   return nullptr;
 }
 
@@ -152,10 +161,13 @@ int dlm_paged_attention_workspace(const dlm_paged_cache* cache, int n_heads, siz
   api_clear_error();
   if (bytes == nullptr) return api_fail(DLM_EINVAL, "paged_attention_workspace: NULL pointer argument");
   if (const char* why = cache_problem(cache)) return api_fail(DLM_EINVAL, why);
-  if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 || n_heads / cache->n_kv_heads > 128)
-    return api_fail(DLM_EINVAL,
-                    "paged_attention: n_heads must be a multiple of n_kv_heads, at most 128 times it");
+  if (const char* why = heads_problem(cache, n_heads)) return api_fail(DLM_EINVAL, why);
   *bytes = 256;
+  if (cache->dtype == DLM_BF16) {
+    PagedDevice* d = nullptr;
+    if (int rc = paged_device(&d)) return rc;
+    *bytes = paged_attention_work(cache->head_dim, d->num_sms);
+  }
   return DLM_OK;
 }
 
@@ -164,8 +176,9 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
                         const int32_t* ctx_lens, const int32_t* block_table, int table_width,
                         int batch, int n_tokens, int n_heads, int mask_block, float scale,
                         void* workspace, size_t workspace_bytes, void* stream) {
-  size_t need = 0;
-  if (int rc = dlm_paged_attention_workspace(cache, n_heads, &need)) return rc;
+  api_clear_error();
+  if (const char* why = cache_problem(cache)) return api_fail(DLM_EINVAL, why);
+  if (const char* why = heads_problem(cache, n_heads)) return api_fail(DLM_EINVAL, why);
   if (n_tokens < 0 || batch < 1 || batch > kPagedMaxBatch || table_width < 1 || mask_block < 0 ||
       !(scale >= 0.f) || !(scale <= 3.0e38f))
     return api_fail(DLM_EINVAL,
@@ -174,8 +187,8 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
   if (n_tokens == 0) return DLM_OK;
   if (!q || !o || !cu_q || !ctx_lens || !block_table || !workspace)
     return api_fail(DLM_EINVAL, "paged_attention: NULL pointer argument");
-  if (workspace_bytes < need || !aligned(workspace, 256))
-    return api_fail(DLM_EINVAL, "paged_attention: the workspace is too small or not 256-byte aligned");
+  if (!aligned(workspace, 256))
+    return api_fail(DLM_EINVAL, "paged_attention: the workspace is not 256-byte aligned");
   const PagedKV c = kv_of(cache);
   const int64_t row = (int64_t)n_heads * c.Dh;
   if (const char* why = rows_problem(q, q_stride, row, c.esize, n_tokens))
@@ -184,9 +197,13 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
     return api_fail(DLM_EINVAL, why);
   if ((long long)n_tokens * n_heads > INT_MAX)
     return api_fail(DLM_EINVAL, "paged_attention: n_tokens * n_heads exceeds 2^31 - 1");
+  if (workspace_bytes < 256)   // the least that any cache needs
+    return api_fail(DLM_EINVAL, "paged_attention: the workspace is too small");
   PagedDevice* d = nullptr;
   int dev = 0;
   if (int rc = paged_device(&d, &dev)) return rc;
+  if (c.esize == 2 && workspace_bytes < paged_attention_work(c.Dh, d->num_sms))
+    return api_fail(DLM_EINVAL, "paged_attention: the workspace is too small");
   for (const void* p : {q, (const void*)o, (const void*)lse, (const void*)cu_q,
                         (const void*)ctx_lens, (const void*)block_table, (const void*)workspace,
                         (const void*)c.k, (const void*)c.v})
@@ -195,7 +212,9 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
   PagedAttn a{c, q, q_stride, o, o_stride, lse, cu_q, ctx_lens, block_table, table_width, batch,
               n_tokens, n_heads, mask_block,
               scale > 0.f ? scale : (float)(1.0 / sqrt((double)c.Dh)), workspace, d->err};
-  if (cudaError_t e = paged_attention_simt(a, (cudaStream_t)stream); e != cudaSuccess)
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = c.esize == 2 ? paged_attention_tc(a, d->num_sms, st) : paged_attention_simt(a, st);
+  if (e != cudaSuccess)
     return api_cuda_fail("paged_attention launch", e);
   return DLM_OK;
 }

@@ -1,0 +1,1034 @@
+// bf16 attention of ragged chunks of new tokens over a paged KV cache.
+//
+// Rows.  The G = H / Hkv query heads of a KV head share its keys: a row tile is
+// npos = floor(128 / G) positions x G heads (row = position * G + head), at
+// most 128 rows = the M of the tensor core's tiles; an item is two
+// consecutive row tiles of a sequence for one KV head.  An item whose second
+// row tile is empty (single tokens, short chunks) gives every other key tile
+// to the second half of the CTA instead, with the same queries.
+//
+// Work.  The grid is persistent, one CTA per SM.  All items, laid end to end in
+// units of keys, are cut into equal ranges, one per CTA, so that one long
+// sequence spreads over all SMs and many short ones share them; lengths are
+// read on the device.  An item that lies in one range is written as bf16; one
+// that is cut leaves float32 partials (unnormalised O, running maximum and
+// sum) in the workspace, which a second kernel joins in a fixed order.
+//
+// Pages.  K and V pages come by TMA as a 5-D box (64 dims, 8 rows, Dh / 64
+// halves, rows / 8 groups, 1 page): whatever the page size (>= 8), a 128-key
+// tile in shared memory is [16 groups of 8 rows][half][8 rows][128 bytes], with
+// one stride between 8-row groups, which is what the MMA descriptors need.
+#include <math_constants.h>
+
+#include "kernels.h"
+
+namespace dlm {
+
+namespace {
+
+constexpr int kKeys = 128;       // keys per tile
+constexpr int kRows = 128;       // rows per row tile
+constexpr int kThreads = 384;    // 12 warps: softmax 0-3 and 4-7, producer, MMA, scheduler, V check
+constexpr int kProducer = 8, kMma = 9, kScheduler = 10, kFixer = 11;
+constexpr int kDescs = 4;
+constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P over S), O0, O1 (Dh each)
+constexpr uint32_t kColO = 256;
+// cost of an item beside its keys, in keys: loading Q, the first S, the epilogue
+constexpr int kItemCost = 128;
+// keys per CTA below which fewer CTAs are used (the join costs more than it saves)
+constexpr int kMinKeys = 256;
+// the running reference of a row moves only when its maximum passes it by
+// more than this (log2 units): P stays below 2^8, O is rarely rescaled
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kRegsSoftmax = 224, kRegsOther = 56;
+static_assert(kRegsSoftmax * 256 + kRegsOther * 128 <= 168 * kThreads,
+              "register split exceeds the launch's registers");
+
+template <int DH>
+struct Tile {
+  static constexpr int kHalves = DH / 64;
+  static constexpr int kGroup = kHalves * 1024;          // 8 rows
+  static constexpr int kBytes = 16 * kGroup;             // a 128-row K or V tile
+  static constexpr int kQHalf = kRows * 128;
+  static constexpr int kQBytes = kHalves * kQHalf;
+  static constexpr int kSlots = DH == 128 ? 5 : 10;      // ring of K and V tiles
+};
+
+struct Item {
+  int b, g;
+  int row0, npos;      // first row of q, positions of the item
+  int pos0, ctx;       // position of the first row, keys of the sequence
+  int ts, te;          // key tiles of this CTA
+  int kt0, pair;       // key tiles of row tile 0; two row tiles
+  int whole;           // every key tile is here: write the result
+  int slot;            // partial slot (1: the item starts here)
+  int fix0;            // first key tile in which some row has a hidden key
+  int poison;          // such a tile holds an infinity or NaN in V
+  int valid;           // 0: no more items
+  int pad;
+};
+static_assert(sizeof(Item) == 64, "");
+
+// what the join needs to know of a CTA's cut items
+struct Meta {
+  int tail;            // an item starts here and is cut
+  int row0, npos, g, pair;
+  int head;            // a partial of an item that started earlier
+  int head_ends;       // ... whose last key tile is here
+  int pad;
+};
+
+template <int DH>
+struct Smem {
+  static constexpr int kQ = 0;
+  static constexpr int kRing = 2 * Tile<DH>::kQBytes;
+  static constexpr int kTail = kRing + Tile<DH>::kSlots * Tile<DH>::kBytes;
+  struct Rest {
+    Item item[kDescs];
+    float2 xml[2][kRows];   // (max, sum) of the second half, alternating between items
+    uint64_t full[Tile<DH>::kSlots], empty[Tile<DH>::kSlots];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t d_full[kDescs], d_empty[kDescs];
+    uint64_t x_full[2], fix_req, fix_done, fin;
+    int start[4], stop[4];
+    uint32_t tmem;
+    int abort;
+  };
+  static constexpr int kBytes = kTail + (int)sizeof(Rest);
+};
+static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory");
+
+struct Params {
+  const int32_t* cu;
+  const int32_t* ctx;
+  const int32_t* table;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* o;
+  int64_t o_stride;
+  float* lse;
+  float* part;         // [cta][2][2 * kRows][DH]
+  float2* ml;          // [cta][2][2 * kRows]
+  Meta* meta;          // [cta]
+  int* err;
+  int W, B, T, H, Hkv, G, npos, block, n_pages, page_shift;
+  float scale_log2;
+};
+
+// matrix descriptors of a 128-row tile whose 8-row groups are `group` bytes
+// apart (128-byte swizzle): K-major (rows = N), and MN-major (rows = K, 64-element
+// chunks of N 1024 bytes apart)
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr, int group) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(group >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, int group) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(1024 >> 4) << 16 |
+         (uint64_t)(group >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int group, int plane) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(plane), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// keys [0, n) that the row at position p sees
+__device__ __forceinline__ int visible(int p, int ctx, int block) {
+  if (block == 0) return ctx;
+  if (p < 0) return 0;
+  if (block == 1) return min(ctx, p + 1);
+  return (int)min((long long)ctx, ((long long)(p / block) + 1) * block);
+}
+
+// The cost of a sequence's items, in keys: item j (2 * npos positions) costs the
+// keys below its last row's position (its block's end is not counted) plus
+// kItemCost.  cum(j) is the cost of the items before j.
+struct SeqCost {
+  long long base;   // position of row 0
+  int n, ctx, pp, items, j0;
+  bool masked;
+  __device__ SeqCost(int n_, int ctx_, int pp_, int block)
+      : base((long long)ctx_ - n_), n(n_), ctx(ctx_), pp(pp_), masked(block != 0) {
+    items = (int)(((long long)n + pp - 1) / pp);
+    // items wholly before position 0 (masked, base < 0): no keys
+    j0 = base < 0 ? min(max(items - 1, 0), (int)(-base / pp)) : 0;
+  }
+  __device__ long long cum(int j) const {
+    if (!masked) return (long long)j * (ctx + kItemCost);
+    const bool end = j == items && j > 0;
+    if (end) --j;
+    long long c = (long long)kItemCost * j;
+    if (j > j0)
+      c += (j - j0) * base +
+           (long long)pp * (((long long)j * (j + 1) - (long long)j0 * (j0 + 1)) / 2);
+    if (end) c += ctx + kItemCost;
+    return c;
+  }
+};
+
+__device__ __forceinline__ bool seq_ok(const Params& p, int c0, int c1, int ctx) {
+  return c0 >= 0 && c0 <= c1 && c1 <= p.T && ctx >= 0 &&
+         (long long)ctx <= ((long long)p.W << p.page_shift);
+}
+
+__device__ __forceinline__ float fmax3f(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float row_max(const float (&sv)[kKeys]) {
+  float m[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m[k] = fmaxf(sv[k], sv[k + 8]);
+#pragma unroll
+  for (int j = 16; j < kKeys; j += 16)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m[k] = fmax3f(m[k], sv[j + k], sv[j + 8 + k]);
+  return fmax3f(fmax3f(m[0], m[1], m[2]), fmax3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+}
+
+// bf16 pair: is either an infinity or NaN?
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  return (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u;
+}
+
+// Adds to o (32 columns from c0) the non-finite V elements of keys
+// [k0, k1): the V check set them to zero in shared memory, so that rows that
+// do not see those keys stay clean.
+template <int DH>
+__device__ __noinline__ void add_poison(const Params& p, const Item& it, int k0, int k1, int c0,
+                                        float (&o)[32]) {
+  const int mask = (1 << p.page_shift) - 1;
+  for (int k = k0; k < k1; ++k) {
+    const int page = p.table[(size_t)it.b * p.W + (k >> p.page_shift)];
+    if (page < 0 || page >= p.n_pages) continue;
+    const __nv_bfloat16* row =
+        p.v + ((((size_t)page * p.Hkv + it.g) << p.page_shift) + (k & mask)) * DH + c0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float x = __bfloat162float(row[j]);
+      if (!(fabsf(x) <= 3.4e38f)) o[j] += x;
+    }
+  }
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmQ, const Params p) {
+  using TL = Tile<DH>;
+  constexpr int NS = TL::kSlots;
+  // the tiles' swizzle wants 1024-byte alignment, and there is no room to round up
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) raise_error(p.err, DLM_EBOUNDS);
+    return;
+  }
+  uint8_t* qs = smem + Smem<DH>::kQ;
+  uint8_t* ring = smem + Smem<DH>::kRing;
+  auto& sh = *reinterpret_cast<typename Smem<DH>::Rest*>(smem + Smem<DH>::kTail);
+  volatile int* abort_flag = &sh.abort;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.o_empty[i], 4);
+      mbar_init(&sh.x_full[i], 4);
+    }
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(&sh.d_full[i], 1);
+      mbar_init(&sh.d_empty[i], 11);   // producer, MMA, V check, 8 softmax warps
+    }
+    mbar_init(&sh.fix_req, 1);
+    mbar_init(&sh.fix_done, 1);
+    mbar_init(&sh.fin, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+    tma_prefetch(&tmK);
+    tma_prefetch(&tmV);
+    tma_prefetch(&tmQ);
+  }
+  if (warp == kMma) tmem_alloc(&sh.tmem, kTmemCols);
+
+  // ---- this CTA's range of the work ----
+  // scan of the sequences' costs (consecutive sequences per thread), then the
+  // owners of the range's two ends turn them into (KV head, sequence, item, tile)
+  {
+    long long* scan = reinterpret_cast<long long*>(ring);   // [12] warp sums; free until the first load
+    const int pp = 2 * p.npos;
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), ctx = __ldg(p.ctx + b);
+      if (!seq_ok(p, c0, c1, ctx)) {
+        if (blockIdx.x == 0) raise_error(p.err, DLM_EBOUNDS);
+        continue;
+      }
+      const SeqCost s(c1 - c0, ctx, pp, p.block);
+      mine += s.cum(s.items);
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) scan[warp] = incl;
+    if (tid < 4) sh.start[tid] = sh.stop[tid] = 0;
+    __syncthreads();
+    long long before = 0, w1 = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w == warp) before = w1;
+      w1 += scan[w];
+    }
+    const long long first = before + incl - mine;   // cost before sequence b0
+    const long long total = w1 * p.Hkv;
+    const long long ctas = max(1ll, min((long long)gridDim.x, total / kMinKeys));
+    auto edge = [&](long long k) {
+      return k >= ctas ? total : (total / ctas) * k + (total % ctas) * k / ctas;
+    };
+    const long long u[2] = {edge(blockIdx.x), edge((long long)blockIdx.x + 1)};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      int* dst = e == 0 ? sh.start : sh.stop;
+      if (w1 == 0 || u[e] >= total) {
+        if (tid == 0) dst[0] = p.Hkv;   // the end
+        continue;
+      }
+      const int g = (int)(u[e] / w1);
+      long long r = u[e] - g * w1 - first;
+      if (r < 0 || r >= mine) continue;
+      for (int b = b0; b < b1; ++b) {
+        const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), ctx = __ldg(p.ctx + b);
+        if (!seq_ok(p, c0, c1, ctx)) continue;
+        const SeqCost s(c1 - c0, ctx, pp, p.block);
+        const long long c = s.cum(s.items);
+        if (r >= c) {
+          r -= c;
+          continue;
+        }
+        int lo = 0, hi = s.items;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s.cum(mid) <= r)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        const long long at = r - s.cum(lo), cost = s.cum(lo + 1) - s.cum(lo);
+        const int i1 = (int)min((long long)s.n, (long long)(lo + 1) * pp);
+        const int kt = (visible(ctx - s.n + i1 - 1, ctx, p.block) + kKeys - 1) / kKeys;
+        dst[0] = g;
+        dst[1] = b;
+        dst[2] = lo;
+        dst[3] = (int)(at * kt / cost);   // < kt; 0: the item starts in this range
+        break;
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp >= kProducer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kProducer) {
+      // ---------------- producer: Q, K and V tiles ----------------
+      uint32_t e = 0;        // ring entries issued (K, V, K, V, ...)
+      uint32_t qn = 0;       // Q tiles issued
+      bool ok = true;
+      const int pages_tile = p.page_shift >= 7 ? 1 : kKeys >> p.page_shift;
+      const int page_bytes = TL::kBytes / pages_tile;
+      for (uint32_t n = 0; ok; ++n) {
+        const int ds = n % kDescs;
+        if (!mbar_wait_bounded(&sh.d_full[ds], (n / kDescs) & 1, abort_flag)) break;
+        const Item& it = sh.item[ds];
+        if (!it.valid) break;
+        const int b = it.b, g = it.g, ts = it.ts, te = it.te, ctx = it.ctx;
+        const int row0 = it.row0, q_tiles = ts == te ? 0 : it.pair ? 2 : 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.d_empty[ds]);
+        const int32_t* row = p.table + (size_t)b * p.W;
+        const int n_pages = (ctx + (1 << p.page_shift) - 1) >> p.page_shift;
+        int chunk = -1, id = 0, id_next = 0;
+        auto load_ids = [&](int c) {
+          const int i = c * 32 + lane;
+          return i < n_pages ? __ldg(row + i) : 0;
+        };
+        for (int t = ts; t < te && ok; ++t) {
+          // page ids, 32 at a time, the next 32 on their way
+          const int page0 = (int)(((long long)t * kKeys) >> p.page_shift);
+          if (page0 >> 5 != chunk) {
+            const int c = page0 >> 5;
+            id = c == chunk + 1 && chunk >= 0 ? id_next : load_ids(c);
+            id_next = load_ids(c + 1);
+            chunk = c;
+          }
+          int page = __shfl_sync(0xffffffffu, id, (page0 + lane) & 31);
+          const bool mine = lane < pages_tile && page0 + lane < n_pages;
+          if (mine && (page < 0 || page >= p.n_pages)) {
+            raise_error(p.err, DLM_EBOUNDS);
+            page = p.n_pages;   // outside the map: zeros
+          }
+          const int plane = page * p.Hkv + g;
+          const int group = p.page_shift > 7 ? (t & ((1 << (p.page_shift - 7)) - 1)) * 16 : 0;
+          const uint32_t bytes = (uint32_t)(min(pages_tile, n_pages - page0) * page_bytes);
+          if (t == ts) {
+            // the item's queries first
+            for (int i = 0; i < q_tiles && ok; ++i, ++qn) {
+              const int qslot = qn & 1;
+              ok = mbar_wait_bounded(&sh.q_empty[qslot], ((qn >> 1) & 1) ^ 1, abort_flag);
+              if (ok && lane == 0) {
+                mbar_arrive_expect_tx(&sh.q_full[qslot], (uint32_t)(p.npos * p.G * DH * 2));
+                for (int h = 0; h < TL::kHalves; ++h)
+                  tma_load_3d(qs + qslot * TL::kQBytes + h * TL::kQHalf, &tmQ, &sh.q_full[qslot],
+                              h * 64, g * p.G, row0 + i * p.npos);
+              }
+            }
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int slot = e % NS;
+            if (!mbar_wait_bounded(&sh.empty[slot], ((e / NS) & 1) ^ 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+            __syncwarp();
+            if (mine)
+              tma_load_5d(ring + slot * TL::kBytes + lane * page_bytes, kv == 0 ? &tmK : &tmV,
+                          &sh.full[slot], group, plane);
+            ++e;
+          }
+        }
+      }
+      if (*abort_flag) {
+        // the copies in flight land before the CTA exits
+        for (uint32_t k = e > NS ? e - NS : 0; k < e; ++k)
+          mbar_wait_bounded(&sh.full[k % NS], (k / NS) & 1, nullptr);
+        for (uint32_t k = qn > 2 ? qn - 2 : 0; k < qn; ++k)
+          mbar_wait_bounded(&sh.q_full[k & 1], (k >> 1) & 1, nullptr);
+      }
+    } else if (warp == kMma) {
+      // ---------------- MMA issuer ----------------
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DH, true);
+        uint32_t eb = 0;               // ring entry of the item's first K
+        uint32_t ready = 0;            // ring entries known to be full, in order
+        uint32_t qn = 0;               // Q tiles used
+        uint32_t np[2] = {0, 0};       // P tiles consumed
+        uint32_t no[2] = {0, 0};       // O accumulations started
+        uint32_t asked = 0, fixed = 0; // V checks asked for, known to be done
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+          const int ds = n % kDescs;
+          if (!mbar_wait_bounded(&sh.d_full[ds], (n / kDescs) & 1, abort_flag)) break;
+          const Item& it = sh.item[ds];
+          if (!it.valid) break;
+          const int L = it.te - it.ts;
+          const bool pair = it.pair != 0;
+          const int c0 = pair ? max(0, min(L, it.kt0 - it.ts)) : (L + 1) >> 1;
+          const int c1 = pair ? L : L >> 1;
+          const int fix_l = max(0, it.fix0 - it.ts);   // first local tile to be checked
+          mbar_arrive(&sh.d_empty[ds]);
+          if (L == 0) continue;
+          const uint32_t q0 = qn, q1 = pair ? qn + 1 : qn;
+          ok = mbar_wait_bounded(&sh.q_full[q0 & 1], (q0 >> 1) & 1, abort_flag) &&
+               mbar_wait_bounded(&sh.q_full[q1 & 1], (q1 >> 1) & 1, abort_flag);
+          const uint32_t fix_base = fixed;   // checks of earlier items
+          int s0 = 0, s1 = 0, v0 = 0, v1 = 0;   // S and P V tiles issued per row tile
+          uint64_t t_idle = 0;
+          for (uint32_t spin = 0; ok && (v0 < c0 || v1 < c1); ++spin) {
+            bool progress = false;
+            while (ready < eb + 2 * L && mbar_test_wait(&sh.full[ready % NS], (ready / NS) & 1)) ++ready;
+            // one V check at a time: the next checked tile's V is there
+            if (asked - fix_base < (uint32_t)(L - min(L, fix_l)) && asked == fixed &&
+                ready > eb + 2 * (fix_l + (asked - fix_base)) + 1) {
+              mbar_arrive(&sh.fix_req);
+              ++asked;
+            }
+            if (fixed < asked && mbar_test_wait(&sh.fix_done, fixed & 1)) {
+              ++fixed;
+              progress = true;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              int& s = i == 0 ? s0 : s1;
+              int& v = i == 0 ? v0 : v1;
+              const int c = i == 0 ? c0 : c1;
+              const int l = pair ? s : 2 * s + i;
+              if (s < c && s == v && ready > eb + 2 * l) {
+                tc_fence_after();
+                const uint32_t en = eb + 2 * l;
+                const uint32_t qa = smem_u32(qs + ((i == 0 ? q0 : q1) & 1) * TL::kQBytes);
+                const uint32_t ka = smem_u32(ring + (en % NS) * TL::kBytes);
+#pragma unroll
+                for (int k = 0; k < DH / 16; ++k)
+                  umma_bf16(tmem + i * kKeys, sw128_desc(qa + (k >> 2) * TL::kQHalf + (k & 3) * 32),
+                            desc_k(ka + (k >> 2) * 1024 + (k & 3) * 32, TL::kGroup), idesc_s, k > 0);
+                umma_commit(&sh.s_full[i]);
+                ++s;
+                // K is free once every row tile that needs it has its S issued
+                if (!pair || (s1 > l && (l >= c0 || s0 > l))) umma_commit(&sh.empty[en % NS]);
+                // Q likewise
+                if (pair) {
+                  if (s == c) umma_commit(&sh.q_empty[(i == 0 ? q0 : q1) & 1]);
+                } else if (s0 == c0 && s1 == c1) {
+                  umma_commit(&sh.q_empty[q0 & 1]);
+                }
+                progress = true;
+              }
+              const int lv = pair ? v : 2 * v + i;
+              if (v < s && ready > eb + 2 * lv + 1 &&
+                  (lv < fix_l || fixed - fix_base > (uint32_t)(lv - fix_l)) &&
+                  mbar_test_wait(&sh.p_full[i], np[i] & 1) &&
+                  (v > 0 || mbar_test_wait(&sh.o_empty[i], (no[i] & 1) ^ 1))) {
+                tc_fence_after();
+                const uint32_t en = eb + 2 * lv + 1;
+                const uint32_t va = smem_u32(ring + (en % NS) * TL::kBytes);
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                  umma_bf16_tmem_a(tmem + kColO + i * 128, tmem + i * kKeys + k * 8,
+                                   desc_mn(va + k * 2 * TL::kGroup, TL::kGroup), idesc_o,
+                                   v > 0 || k > 0);
+                if (v == 0) ++no[i];
+                ++np[i];
+                ++v;
+                if (!pair || (v1 > lv && (lv >= c0 || v0 > lv))) umma_commit(&sh.empty[en % NS]);
+                if (v == c) umma_commit(&sh.o_full[i]);
+                progress = true;
+              }
+            }
+            if (progress) {
+              t_idle = 0;
+              continue;
+            }
+            // nothing ready: sleep briefly on the P that has been waited for longest
+            const int w = v0 < s0 && (v1 >= s1 || v0 <= v1) ? 0 : 1;
+            if ((w == 0 ? v0 < s0 : v1 < s1))
+              mbar_try_wait_hint(&sh.p_full[w], np[w] & 1, 200u);
+            if ((spin & 255u) == 0) {
+              if (*abort_flag) {
+                ok = false;
+                break;
+              }
+              const uint64_t now = global_ns();
+              if (t_idle == 0) {
+                t_idle = now;
+              } else if (now - t_idle > kWaitLimitNs) {
+                *abort_flag = 1;
+                ok = false;
+              }
+            }
+          }
+          // a row tile without keys here (pair, c0 == 0) never used its Q
+          if (ok && pair && c0 == 0) umma_commit(&sh.q_empty[q0 & 1]);
+          eb += 2 * L;
+          qn += pair ? 2 : 1;
+        }
+        umma_commit(&sh.fin);   // every MMA issued has finished
+        mbar_wait_bounded(&sh.fin, 0, nullptr);
+      }
+    } else if (warp == kScheduler) {
+      // ---------------- scheduler: the range's items, one descriptor each ----------------
+      const int g1 = sh.stop[0], b_end = sh.stop[1], j_end = sh.stop[2], t_end = sh.stop[3];
+      int g = sh.start[0], b = sh.start[1], j = sh.start[2], t0 = sh.start[3];
+      Meta meta = {};
+      int cb = -1;   // 32 sequences in registers, one per lane
+      int l0 = 0, l1 = 0, lc = 0;
+      uint32_t n = 0;
+      bool ok = true;
+      for (;;) {
+        bool more = g < g1 || (g == g1 && g < p.Hkv && (b < b_end || (b == b_end && (j < j_end ||
+                                                        (j == j_end && t_end > 0)))));
+        Item it = {};
+        if (more) {
+          if (b >> 5 != cb) {
+            cb = b >> 5;
+            const int bb = cb * 32 + lane;
+            const bool in = bb < p.B;
+            l0 = in ? __ldg(p.cu + bb) : 0;
+            l1 = in ? __ldg(p.cu + bb + 1) : 0;
+            lc = in ? __ldg(p.ctx + bb) : 0;
+            if (!in || !seq_ok(p, l0, l1, lc)) l1 = l0 = 0;
+          }
+          const int c0 = __shfl_sync(0xffffffffu, l0, b & 31);
+          const int c1 = __shfl_sync(0xffffffffu, l1, b & 31);
+          const int ctx = __shfl_sync(0xffffffffu, lc, b & 31);
+          const int len = c1 - c0, pp = 2 * p.npos;
+          if ((long long)j * pp >= len) {   // the next sequence, then the next KV head
+            j = 0;
+            t0 = 0;
+            // over empty sequences of this chunk at once
+            const uint32_t full = __ballot_sync(0xffffffffu, l1 > l0);
+            const uint32_t later = (b & 31) == 31 ? 0u : full & (0xffffffffu << ((b & 31) + 1));
+            b = later != 0 ? (b & ~31) + __ffs(later) - 1 : (b & ~31) + 32;
+            if (b >= p.B) {
+              b = 0;
+              ++g;
+            }
+            continue;
+          }
+          const int i0 = j * pp;
+          it.b = b;
+          it.g = g;
+          it.row0 = c0 + i0;
+          it.npos = min(pp, len - i0);
+          it.pos0 = ctx - len + i0;
+          it.ctx = ctx;
+          it.pair = it.npos > p.npos;
+          const int last0 = it.pos0 + min(it.npos, p.npos) - 1;
+          it.kt0 = (visible(last0, ctx, p.block) + kKeys - 1) / kKeys;
+          const int kt = (visible(it.pos0 + it.npos - 1, ctx, p.block) + kKeys - 1) / kKeys;
+          const bool stops = g == g1 && b == b_end && j == j_end;
+          it.ts = t0;
+          it.te = stops ? t_end : kt;
+          it.whole = it.ts == 0 && it.te == kt;
+          it.slot = it.ts == 0;
+          it.fix0 = visible(it.pos0, ctx, p.block) / kKeys;
+          it.valid = 1;
+          const bool empty_cut = !it.whole && it.ts >= it.te;   // nothing of a cut item
+          if (!it.whole) {
+            if (it.ts == 0) {
+              meta.tail = 1;
+              meta.row0 = it.row0;
+              meta.npos = it.npos;
+              meta.g = g;
+              meta.pair = it.pair;
+            } else {
+              meta.head = !empty_cut;
+              meta.head_ends = it.te == kt;
+            }
+          }
+          t0 = 0;
+          ++j;
+          if (empty_cut) continue;
+        }
+        const int ds = n % kDescs;
+        if (!mbar_wait_bounded(&sh.d_empty[ds], ((n / kDescs) & 1) ^ 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          sh.item[ds] = it;
+          mbar_arrive(&sh.d_full[ds]);
+        }
+        ++n;
+        if (!more) break;
+      }
+      (void)ok;
+      if (lane == 0) p.meta[blockIdx.x] = meta;
+    } else {
+      // ---------------- V check of tiles with hidden keys ----------------
+      // A hidden key has probability 0, but 0 x infinity is NaN: rows behind the
+      // sequence become zero, and so do non-finite elements (the epilogue adds
+      // them to the rows that see them).
+      uint32_t eb = 0, done = 0;
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        const int ds = n % kDescs;
+        if (!mbar_wait_bounded(&sh.d_full[ds], (n / kDescs) & 1, abort_flag)) break;
+        Item& it = sh.item[ds];
+        if (!it.valid) break;
+        const int ts = it.ts, te = it.te, ctx = it.ctx;
+        for (int t = max(ts, it.fix0); t < te; ++t) {
+          if (!mbar_wait_bounded(&sh.fix_req, done & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t en = eb + 2 * (t - ts) + 1;
+          mbar_wait_bounded(&sh.full[en % NS], (en / NS) & 1, abort_flag);   // complete already
+          uint8_t* tile = ring + (en % NS) * TL::kBytes;
+          const int live = ctx - t * kKeys;   // rows of the tile that hold tokens
+          bool bad = false;
+          // 16 bytes at a time; rows are 128 bytes, kHalves per 8-row group
+#pragma unroll 8
+          for (int x = lane; x < TL::kBytes / 16; x += 32) {
+            const int r = (x * 16 / TL::kGroup) * 8 + ((x >> 3) & 7);
+            uint4* at = reinterpret_cast<uint4*>(tile + x * 16);
+            if (r >= live) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else {
+              uint4 w = *at;
+              uint32_t* c = &w.x;
+              bool hit = false;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) hit |= nonfinite2(c[y]);
+              if (hit) {
+                bad = true;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  if ((c[y] & 0x7F800000u) == 0x7F800000u) c[y] &= 0x0000FFFFu;
+                  if ((c[y] & 0x7F80u) == 0x7F80u) c[y] &= 0xFFFF0000u;
+                }
+                *at = w;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          if (__any_sync(0xffffffffu, bad) && lane == 0) it.poison = 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.fix_done);
+          ++done;
+        }
+        eb += 2 * (te - ts);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.d_empty[ds]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ---------------- softmax and epilogue: one row per thread ----------------
+    const int i = warp >> 2;                          // row tile
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t s_col = lane_addr + i * kKeys;
+    const uint32_t o_col = lane_addr + kColO;
+    const int rp = row / p.G, rh = row - rp * p.G;    // position and head of the row
+    uint32_t ns = 0;                                  // S tiles taken
+    uint32_t no[2] = {0, 0};                          // O accumulations finished
+    uint32_t nx = 0;                                  // exchanges of (max, sum)
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      const int ds = n % kDescs;
+      if (!mbar_wait_bounded(&sh.d_full[ds], (n / kDescs) & 1, abort_flag)) break;
+      const Item& it = sh.item[ds];
+      if (!it.valid) break;
+      const bool pair = it.pair != 0;
+      const int L = it.te - it.ts;
+      const int c0 = pair ? max(0, min(L, it.kt0 - it.ts)) : (L + 1) >> 1;
+      const int c1 = pair ? L : L >> 1;
+      const int c = i == 0 ? c0 : c1;
+      const int pos = pair ? i * p.npos + rp : rp;
+      const bool live = rp < p.npos && pos < it.npos;
+      const int lim = live ? visible(it.pos0 + pos, it.ctx, p.block) : 0x7fffffff;
+      const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+      const bool any = __any_sync(0xffffffffu, live);
+      float m_run = -CUDART_INF_F, l_run = 0.f;
+      for (int x = 0; x < c; ++x, ++ns) {
+        const int t = it.ts + (pair ? x : 2 * x + i);
+        if (!mbar_wait_bounded(&sh.s_full[i], ns & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (any) {   // warps without rows leave their lanes of P as they are
+          float sv[kKeys];
+          {
+            uint32_t raw[kKeys / 32][32];
+#pragma unroll
+            for (int y = 0; y < kKeys / 32; ++y) tmem_ld32_nowait(s_col + y * 32, raw[y]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < kKeys / 32; ++y)
+#pragma unroll
+              for (int z = 0; z < 32; ++z) sv[y * 32 + z] = __uint_as_float(raw[y][z]);
+          }
+          const int left = lim - t * kKeys;
+          if (lim_min - t * kKeys < kKeys) {
+#pragma unroll
+            for (int z = 0; z < kKeys; ++z)
+              if (z >= left) sv[z] = -CUDART_INF_F;
+          }
+          const float mx = row_max(sv) * p.scale_log2;
+          const bool move = __any_sync(0xffffffffu, mx > m_run + kRescaleLog2);
+          const float m_new = move ? fmaxf(m_run, mx) : m_run;
+          const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // no key seen yet
+          const float alpha = move ? fast_exp2(m_run - base) : 1.f;
+          float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int y = 0; y < kKeys / 32; ++y) {
+            uint32_t w[16];
+#pragma unroll
+            for (int z = 0; z < 16; ++z) {
+              const float e0 = fast_exp2(fmaf(sv[32 * y + 2 * z], p.scale_log2, -base));
+              const float e1 = fast_exp2(fmaf(sv[32 * y + 2 * z + 1], p.scale_log2, -base));
+              rs[z & 7] += e0 + e1;
+              w[z] = pack_bf16(e0, e1);   // the MMA's operand type; the sum keeps float32
+            }
+            tmem_st16_u(s_col + y * 16, w);
+          }
+          l_run = l_run * alpha +
+                  (((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7])));
+          m_run = m_new;
+          // S(x) was issued after P(x-1) V, so O holds every earlier tile
+          if (x > 0 && move) {
+#pragma unroll 1
+            for (int y = 0; y < DH / 32; ++y) {
+              float o[32];
+              tmem_ld32(o_col + i * 128 + y * 32, o);
+#pragma unroll
+              for (int z = 0; z < 32; ++z) o[z] *= alpha;
+              tmem_st32(o_col + i * 128 + y * 32, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[i]);
+      }
+      if (!ok) break;
+      // ---- epilogue ----
+      const int nr = pair ? i * kRows + row : row;   // row of the item
+      if (!pair && c1 > 0) {
+        if (i == 1) {
+          // two buffers: this half can be one item ahead of the other's
+          // epilogue, not two (its P V waits for o_empty)
+          sh.xml[nx & 1][row] = make_float2(m_run, l_run);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.x_full[nx & 1]);
+        } else if (!mbar_wait_bounded(&sh.x_full[nx & 1], (nx >> 1) & 1, abort_flag)) {
+          break;
+        }
+        ++nx;
+      }
+      if (pair || i == 0) {
+        float w0 = 1.f, w1 = 0.f;
+        const bool two = !pair && c1 > 0;
+        if (c > 0 && !mbar_wait_bounded(&sh.o_full[i], no[i] & 1, abort_flag)) break;
+        if (two) {
+          if (!mbar_wait_bounded(&sh.o_full[1], no[1] & 1, abort_flag)) break;
+          const float2 x = sh.xml[(nx & 1) ^ 1][row];
+          const float mm = fmaxf(m_run, x.x);
+          w0 = m_run == -CUDART_INF_F ? 0.f : fast_exp2(m_run - mm);
+          w1 = x.x == -CUDART_INF_F ? 0.f : fast_exp2(x.x - mm);
+          l_run = l_run * w0 + x.y * w1;
+          m_run = mm;
+        }
+        tc_fence_after();
+        const bool poison = it.poison != 0;
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        const size_t prow = ((size_t)blockIdx.x * 2 + it.slot) * (2 * kRows) + nr;
+        const int64_t grow = (int64_t)it.row0 + pos;
+        const int head = it.g * p.G + rh;
+        if (any) {
+#pragma unroll 1
+          for (int y = 0; y < DH / 32; ++y) {
+            float o[32];
+            if (c > 0) {
+              tmem_ld32(o_col + i * 128 + y * 32, o);
+            } else {
+#pragma unroll
+              for (int z = 0; z < 32; ++z) o[z] = 0.f;
+            }
+            if (two) {
+              float o1[32];
+              tmem_ld32(o_col + 128 + y * 32, o1);
+#pragma unroll
+              for (int z = 0; z < 32; ++z) o[z] = o[z] * w0 + o1[z] * w1;
+            }
+            if (!live) continue;
+            if (poison) {
+              float x[32];
+#pragma unroll
+              for (int z = 0; z < 32; ++z) x[z] = o[z];
+              add_poison<DH>(p, it, max(it.ts, it.fix0) * kKeys, min(lim, it.te * kKeys), y * 32, x);
+#pragma unroll
+              for (int z = 0; z < 32; ++z) o[z] = x[z];
+            }
+            if (it.whole) {
+              uint4* dst = reinterpret_cast<uint4*>(p.o + grow * p.o_stride + (int64_t)head * DH + y * 32);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                uint4 w;
+                w.x = pack_bf16(o[8 * z] * inv, o[8 * z + 1] * inv);
+                w.y = pack_bf16(o[8 * z + 2] * inv, o[8 * z + 3] * inv);
+                w.z = pack_bf16(o[8 * z + 4] * inv, o[8 * z + 5] * inv);
+                w.w = pack_bf16(o[8 * z + 6] * inv, o[8 * z + 7] * inv);
+                dst[z] = w;
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.part + prow * DH + y * 32);
+#pragma unroll
+              for (int z = 0; z < 8; ++z)
+                dst[z] = make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+            }
+          }
+          if (live) {
+            if (!it.whole)
+              p.ml[prow] = make_float2(m_run, l_run);
+            else if (p.lse != nullptr)
+              p.lse[(size_t)grow * p.H + head] =
+                  l_run == 0.f ? -CUDART_INF_F : (m_run + log2f(l_run)) * 0.69314718055994531f;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (c > 0) mbar_arrive(&sh.o_empty[i]);
+          if (two) mbar_arrive(&sh.o_empty[1]);
+        }
+      }
+      no[0] += c0 > 0;
+      no[1] += c1 > 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.d_empty[ds]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (tid == 0 && *abort_flag) raise_error(p.err, DLM_ETIMEOUT);
+}
+
+// Joins the partials of an item that starts in CTA c: c's own, then those of
+// c + 1, ... up to the CTA where it ends, in that order.  One warp per row,
+// lane = DH / 32 columns.
+template <int DH>
+__global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_ctas) {
+  constexpr int E = DH / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Meta me = p.meta[c];
+  if (!me.tail) return;
+  const int rows = me.pair ? 2 * kRows : kRows;
+  if ((int)blockIdx.y * 32 >= rows) return;
+  // the CTA where the item ends
+  int last = c;
+  for (int k0 = c + 1; k0 < n_ctas; k0 += 32) {
+    const int k = k0 + lane;
+    const bool ends = k < n_ctas && p.meta[k].head_ends != 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, ends);
+    if (m != 0) {
+      last = k0 + __ffs(m) - 1;
+      break;
+    }
+  }
+  for (int r = blockIdx.y * 32 + warp; r < min(rows, (int)blockIdx.y * 32 + 32); r += 8) {
+    const int tile = r / kRows, x = r - tile * kRows;
+    const int rp = x / p.G, rh = x - rp * p.G, pos = tile * p.npos + rp;
+    if (rp >= p.npos || pos >= me.npos) continue;
+    float m = -CUDART_INF_F;
+    for (int k = c + lane; k <= last; k += 32)
+      if (k == c || p.meta[k].head) m = fmaxf(m, p.ml[((size_t)k * 2 + (k == c)) * (2 * kRows) + r].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float l = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int k = c; k <= last; ++k) {
+      if (k != c && !p.meta[k].head) continue;
+      const size_t at = ((size_t)k * 2 + (k == c)) * (2 * kRows) + r;
+      const float2 v = p.ml[at];
+      if (v.x == -CUDART_INF_F) continue;
+      const float w = fast_exp2(v.x - m);
+      l += v.y * w;
+      if (w == 0.f) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += w * p.part[at * DH + lane * E + e];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t grow = (int64_t)me.row0 + pos;
+    const int head = me.g * p.G + rh;
+    __nv_bfloat16* dst = p.o + grow * p.o_stride + (int64_t)head * DH + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+    if (p.lse != nullptr && lane == 0)
+      p.lse[(size_t)grow * p.H + head] =
+          l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool encode(CUtensorMap* m, void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(api_encode_tiled());
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return fn != nullptr &&
+         fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, base, dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t part_bytes(int ctas, int Dh) { return (size_t)ctas * 2 * 2 * kRows * Dh * sizeof(float); }
+size_t ml_bytes(int ctas) { return (size_t)ctas * 2 * 2 * kRows * sizeof(float2); }
+
+template <int DH>
+cudaError_t launch(const PagedAttn& a, int num_sms, cudaStream_t st) {
+  static DeviceOnce once;
+  cudaError_t e = once.get([] {
+    return cudaFuncSetAttribute(paged_attn_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Smem<DH>::kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  Params p;
+  p.cu = a.cu;
+  p.ctx = a.ctx;
+  p.table = a.table;
+  p.v = (const __nv_bfloat16*)a.c.v;
+  p.o = (__nv_bfloat16*)a.o;
+  p.o_stride = a.o_stride;
+  p.lse = a.lse;
+  uint8_t* work = (uint8_t*)a.work;
+  p.part = (float*)work;
+  p.ml = (float2*)(work + part_bytes(num_sms, DH));
+  p.meta = (Meta*)(work + part_bytes(num_sms, DH) + ml_bytes(num_sms));
+  p.err = a.err;
+  p.W = a.W;
+  p.B = a.B;
+  p.T = a.T;
+  p.H = a.H;
+  p.Hkv = a.c.Hkv;
+  p.G = a.H / a.c.Hkv;
+  p.npos = kRows / p.G;
+  p.block = a.block;
+  p.n_pages = a.c.n_pages;
+  p.page_shift = a.c.page_shift;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+
+  const cuuint64_t rows = (cuuint64_t)1 << a.c.page_shift;
+  const cuuint64_t kd[5] = {64, 8, DH / 64, rows / 8, (cuuint64_t)a.c.n_pages * a.c.Hkv};
+  const cuuint64_t ks[4] = {DH * 2, 128, DH * 16, rows * DH * 2};
+  const cuuint32_t kb[5] = {64, 8, DH / 64, (cuuint32_t)(rows < kKeys ? rows : kKeys) / 8, 1};
+  const cuuint64_t qd[3] = {DH, (cuuint64_t)a.H, (cuuint64_t)a.T};
+  const cuuint64_t qst[2] = {DH * 2, (cuuint64_t)a.q_stride * 2};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.npos};
+  CUtensorMap tmK, tmV, tmQ;
+  if (!encode(&tmK, a.c.k, 5, kd, ks, kb) || !encode(&tmV, a.c.v, 5, kd, ks, kb) ||
+      !encode(&tmQ, const_cast<void*>(a.q), 3, qd, qst, qb))
+    return cudaErrorInvalidValue;
+  paged_attn_kernel<DH><<<num_sms, kThreads, Smem<DH>::kBytes, st>>>(tmK, tmV, tmQ, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_pdl(paged_join_kernel<DH>, dim3(num_sms, 2 * kRows / 32), dim3(256), 0, st, p, num_sms);
+}
+
+}  // namespace
+
+size_t paged_attention_work(int Dh, int num_sms) {
+  return part_bytes(num_sms, Dh) + ml_bytes(num_sms) + (size_t)num_sms * sizeof(Meta);
+}
+
+cudaError_t paged_attention_tc(const PagedAttn& a, int num_sms, cudaStream_t st) {
+  return a.c.Dh == 128 ? launch<128>(a, num_sms, st) : launch<64>(a, num_sms, st);
+}
+
+}  // namespace dlm
