@@ -493,10 +493,12 @@ int dlm_check(dlm_ctx *ctx, void *stream);
  * wait returned, 3.. kernel phases (GEMM: first / last ring stage full,
  * first accumulator ready, last epilogue done; attention: query and first
  * K/V tile loaded, O complete, cluster barrier, peers' rows received,
- * combined; commit: rows reduced, keys sorted, done).  The table keeps the
+ * combined; commit: rows reduced, keys sorted, done; paged attention: range
+ * known, first K tile, first S, first P, first O, last item).  The table keeps the
  * last launch of each kind; 0 = not reached.  Kinds: 0 embed, 1 QKV GEMM,
  * 2 QKV epilogue, 3 attention, 4 attention combine, 5 Wo GEMM, 6 Wo
- * epilogue, 7 row quantisation, 8 LM head, 9 commit.  The default build
+ * epilogue, 7 row quantisation, 8 LM head, 9 commit, 10
+ * paged attention, 11 its join.  The default build
  * exports the same calls; they return DLM_ESTATE. */
 
 /* Table dimensions: kinds x ctas (linear CTA index) x slots. */

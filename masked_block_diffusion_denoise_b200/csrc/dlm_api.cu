@@ -1351,7 +1351,7 @@ int dlm_trace_read(unsigned long long* table, size_t words) {
   std::vector<unsigned long long> part(n);
   std::fill(table, table + n, 0ull);
   cudaError_t (*copies[])(unsigned long long*) = {trace_copy_gemm, trace_copy_simt, trace_copy_attn,
-                                                  trace_copy_misc, trace_copy_sel};
+                                                  trace_copy_misc, trace_copy_sel, trace_copy_paged};
   for (auto copy : copies) {
     if (cudaError_t e = copy(part.data()); e != cudaSuccess)
       return cuda_fail(nullptr, "trace_read", e);
@@ -1366,7 +1366,7 @@ int dlm_trace_read(unsigned long long* table, size_t words) {
 int dlm_trace_clear(void) {
 #ifdef DLM_TRACE
   cudaError_t (*clears[])() = {trace_clear_gemm, trace_clear_simt, trace_clear_attn,
-                               trace_clear_misc, trace_clear_sel};
+                               trace_clear_misc, trace_clear_sel, trace_clear_paged};
   for (auto clear : clears)
     if (cudaError_t e = clear(); e != cudaSuccess) return cuda_fail(nullptr, "trace_clear", e);
   if (cudaError_t e = cudaDeviceSynchronize(); e != cudaSuccess)

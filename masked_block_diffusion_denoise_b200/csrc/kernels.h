@@ -51,7 +51,9 @@ enum TraceKind {
   TRACE_QUANTIZE = 7,
   TRACE_LM_HEAD = 8,
   TRACE_COMMIT = 9,
-  TRACE_KINDS_USED = 10
+  TRACE_PAGED = 10,
+  TRACE_PAGED_JOIN = 11,
+  TRACE_KINDS_USED = 12
 };
 #ifdef DLM_TRACE
 // each translation unit's table (see DLM_TRACE_STORAGE)
@@ -65,6 +67,8 @@ cudaError_t trace_copy_misc(unsigned long long* host);
 cudaError_t trace_clear_misc();
 cudaError_t trace_copy_sel(unsigned long long* host);
 cudaError_t trace_clear_sel();
+cudaError_t trace_copy_paged(unsigned long long* host);
+cudaError_t trace_clear_paged();
 #endif
 
 struct GemmIO {

@@ -24,6 +24,8 @@
 
 namespace dlm {
 
+DLM_TRACE_STORAGE(paged)
+
 namespace {
 
 constexpr int kKeys = 128;       // keys per tile
@@ -62,8 +64,8 @@ struct Item {
   int kt0, pair;       // key tiles of row tile 0; two row tiles
   int whole;           // every key tile is here: write the result
   int slot;            // partial slot (1: the item starts here)
-  int fix0;            // first key tile in which some row has a hidden key
-  int poison;          // such a tile holds an infinity or NaN in V
+  int fix;             // keys that every row sees; V behind them is checked
+  int poison;          // ... and holds an infinity or NaN
   int valid;           // 0: no more items
   int pad;
 };
@@ -89,7 +91,7 @@ struct Smem {
     uint64_t full[Tile<DH>::kSlots], empty[Tile<DH>::kSlots];
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
     uint64_t d_full[kDescs], d_empty[kDescs];
-    uint64_t x_full[2], fix_req, fix_done, fin;
+    uint64_t x_full[2], fix_req[2], fix_done[2], fin;
     int start[4], stop[4];
     uint32_t tmem;
     int abort;
@@ -133,6 +135,16 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       " [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(plane), "r"(smem_u32(bar))
       : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
 }
 
 // keys [0, n) that the row at position p sees
@@ -190,11 +202,6 @@ __device__ __forceinline__ float row_max(const float (&sv)[kKeys]) {
   return fmax3f(fmax3f(m[0], m[1], m[2]), fmax3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
-// bf16 pair: is either an infinity or NaN?
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-  return (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u;
-}
-
 // Adds to o (32 columns from c0) the non-finite V elements of keys
 // [k0, k1): the V check set them to zero in shared memory, so that rows that
 // do not see those keys stay clean.
@@ -221,6 +228,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tmQ, const Params p) {
   using TL = Tile<DH>;
   constexpr int NS = TL::kSlots;
+  // timeline marks: 2 range known, 3 first K tile, 4 first S, 5 first P written,
+  // 6 first O complete, 7 last item done
+  DLM_TRACE_CTA(TRACE_PAGED);
   // the tiles' swizzle wants 1024-byte alignment, and there is no room to round up
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {
@@ -246,13 +256,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.o_empty[i], 4);
       mbar_init(&sh.x_full[i], 4);
+      mbar_init(&sh.fix_req[i], 1);
+      mbar_init(&sh.fix_done[i], 1);
     }
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(&sh.d_full[i], 1);
       mbar_init(&sh.d_empty[i], 11);   // producer, MMA, V check, 8 softmax warps
     }
-    mbar_init(&sh.fix_req, 1);
-    mbar_init(&sh.fix_done, 1);
     mbar_init(&sh.fin, 1);
     sh.abort = 0;
     fence_mbar_init();
@@ -345,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  if (tid == 0) DLM_TRACE_MARK(2);
 
   if (warp >= kProducer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -428,125 +439,118 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMma) {
       // ---------------- MMA issuer ----------------
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
-        constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DH, true);
-        uint32_t eb = 0;               // ring entry of the item's first K
-        uint32_t ready = 0;            // ring entries known to be full, in order
-        uint32_t qn = 0;               // Q tiles used
-        uint32_t np[2] = {0, 0};       // P tiles consumed
-        uint32_t no[2] = {0, 0};       // O accumulations started
-        uint32_t asked = 0, fixed = 0; // V checks asked for, known to be done
-        bool ok = true;
-        for (uint32_t n = 0; ok; ++n) {
-          const int ds = n % kDescs;
-          if (!mbar_wait_bounded(&sh.d_full[ds], (n / kDescs) & 1, abort_flag)) break;
-          const Item& it = sh.item[ds];
-          if (!it.valid) break;
-          const int L = it.te - it.ts;
-          const bool pair = it.pair != 0;
-          const int c0 = pair ? max(0, min(L, it.kt0 - it.ts)) : (L + 1) >> 1;
-          const int c1 = pair ? L : L >> 1;
-          const int fix_l = max(0, it.fix0 - it.ts);   // first local tile to be checked
-          mbar_arrive(&sh.d_empty[ds]);
-          if (L == 0) continue;
-          const uint32_t q0 = qn, q1 = pair ? qn + 1 : qn;
-          ok = mbar_wait_bounded(&sh.q_full[q0 & 1], (q0 >> 1) & 1, abort_flag) &&
-               mbar_wait_bounded(&sh.q_full[q1 & 1], (q1 >> 1) & 1, abort_flag);
-          const uint32_t fix_base = fixed;   // checks of earlier items
-          int s0 = 0, s1 = 0, v0 = 0, v1 = 0;   // S and P V tiles issued per row tile
-          uint64_t t_idle = 0;
-          for (uint32_t spin = 0; ok && (v0 < c0 || v1 < c1); ++spin) {
-            bool progress = false;
-            while (ready < eb + 2 * L && mbar_test_wait(&sh.full[ready % NS], (ready / NS) & 1)) ++ready;
-            // one V check at a time: the next checked tile's V is there
-            if (asked - fix_base < (uint32_t)(L - min(L, fix_l)) && asked == fixed &&
-                ready > eb + 2 * (fix_l + (asked - fix_base)) + 1) {
-              mbar_arrive(&sh.fix_req);
-              ++asked;
-            }
-            if (fixed < asked && mbar_test_wait(&sh.fix_done, fixed & 1)) {
-              ++fixed;
-              progress = true;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              int& s = i == 0 ? s0 : s1;
-              int& v = i == 0 ? v0 : v1;
-              const int c = i == 0 ? c0 : c1;
-              const int l = pair ? s : 2 * s + i;
-              if (s < c && s == v && ready > eb + 2 * l) {
-                tc_fence_after();
-                const uint32_t en = eb + 2 * l;
-                const uint32_t qa = smem_u32(qs + ((i == 0 ? q0 : q1) & 1) * TL::kQBytes);
-                const uint32_t ka = smem_u32(ring + (en % NS) * TL::kBytes);
-#pragma unroll
-                for (int k = 0; k < DH / 16; ++k)
-                  umma_bf16(tmem + i * kKeys, sw128_desc(qa + (k >> 2) * TL::kQHalf + (k & 3) * 32),
-                            desc_k(ka + (k >> 2) * 1024 + (k & 3) * 32, TL::kGroup), idesc_s, k > 0);
-                umma_commit(&sh.s_full[i]);
-                ++s;
-                // K is free once every row tile that needs it has its S issued
-                if (!pair || (s1 > l && (l >= c0 || s0 > l))) umma_commit(&sh.empty[en % NS]);
-                // Q likewise
-                if (pair) {
-                  if (s == c) umma_commit(&sh.q_empty[(i == 0 ? q0 : q1) & 1]);
-                } else if (s0 == c0 && s1 == c1) {
-                  umma_commit(&sh.q_empty[q0 & 1]);
-                }
-                progress = true;
-              }
-              const int lv = pair ? v : 2 * v + i;
-              if (v < s && ready > eb + 2 * lv + 1 &&
-                  (lv < fix_l || fixed - fix_base > (uint32_t)(lv - fix_l)) &&
-                  mbar_test_wait(&sh.p_full[i], np[i] & 1) &&
-                  (v > 0 || mbar_test_wait(&sh.o_empty[i], (no[i] & 1) ^ 1))) {
-                tc_fence_after();
-                const uint32_t en = eb + 2 * lv + 1;
-                const uint32_t va = smem_u32(ring + (en % NS) * TL::kBytes);
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  umma_bf16_tmem_a(tmem + kColO + i * 128, tmem + i * kKeys + k * 8,
-                                   desc_mn(va + k * 2 * TL::kGroup, TL::kGroup), idesc_o,
-                                   v > 0 || k > 0);
-                if (v == 0) ++no[i];
-                ++np[i];
-                ++v;
-                if (!pair || (v1 > lv && (lv >= c0 || v0 > lv))) umma_commit(&sh.empty[en % NS]);
-                if (v == c) umma_commit(&sh.o_full[i]);
-                progress = true;
-              }
-            }
-            if (progress) {
-              t_idle = 0;
-              continue;
-            }
-            // nothing ready: sleep briefly on the P that has been waited for longest
-            const int w = v0 < s0 && (v1 >= s1 || v0 <= v1) ? 0 : 1;
-            if ((w == 0 ? v0 < s0 : v1 < s1))
-              mbar_try_wait_hint(&sh.p_full[w], np[w] & 1, 200u);
-            if ((spin & 255u) == 0) {
-              if (*abort_flag) {
-                ok = false;
-                break;
-              }
-              const uint64_t now = global_ns();
-              if (t_idle == 0) {
-                t_idle = now;
-              } else if (now - t_idle > kWaitLimitNs) {
-                *abort_flag = 1;
-                ok = false;
-              }
-            }
-          }
-          // a row tile without keys here (pair, c0 == 0) never used its Q
-          if (ok && pair && c0 == 0) umma_commit(&sh.q_empty[q0 & 1]);
-          eb += 2 * L;
-          qn += pair ? 2 : 1;
+      // One fixed order, no polling: with two row tiles PV0(l) S0(l+1) PV1(l)
+      // S1(l+1), with one PV(l) S(l+2) over alternating halves.  While one half's
+      // softmax runs, the tensor core works for the other.  The whole warp walks
+      // the loop and one elected lane issues: operands that are the same in all
+      // lanes reach the MMA without a move per instruction.
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DH, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t kd0 = desc_k(smem_u32(ring), TL::kGroup);
+      const uint64_t vd0 = desc_mn(smem_u32(ring), TL::kGroup);
+      const uint64_t qd0 = desc_k(smem_u32(qs), 1024);
+      uint32_t ks = 0, kph = 0;      // ring slot and phase of the next S's K
+      uint32_t vs = 1, vph = 0;      // ... of the next P V's V
+      auto advance = [](uint32_t& slot, uint32_t& phase, uint32_t by) {
+        slot += by;
+        if (slot >= NS) {
+          slot -= NS;
+          phase ^= 1;
         }
-        umma_commit(&sh.fin);   // every MMA issued has finished
-        mbar_wait_bounded(&sh.fin, 0, nullptr);
+      };
+      uint32_t qn = 0;               // Q tiles used
+      uint32_t np = 0;               // bit i: phase of the next P of half i
+      uint32_t no = 3;               // bit i: phase of the next wait for an empty O of half i
+      uint32_t fb = 0;               // V checks of earlier items
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        const int ds = n % kDescs;
+        if (!mbar_wait_bounded(&sh.d_full[ds], (n / kDescs) & 1, abort_flag)) break;
+        const Item& it = sh.item[ds];
+        if (!__shfl_sync(0xffffffffu, it.valid, 0)) break;
+        const int L = __shfl_sync(0xffffffffu, it.te - it.ts, 0);
+        const bool pair = __shfl_sync(0xffffffffu, it.pair, 0) != 0;
+        const int c0 = pair ? max(0, min(L, __shfl_sync(0xffffffffu, it.kt0 - it.ts, 0))) : L;
+        const int fix_l = max(0, __shfl_sync(0xffffffffu, it.fix / kKeys - it.ts, 0));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.d_empty[ds]);
+        if (L == 0) continue;
+        const uint32_t q0 = qn & 1, q1 = pair ? q0 ^ 1 : q0;
+        if (!mbar_wait_bounded(&sh.q_full[q0], (qn >> 1) & 1, abort_flag) ||
+            (pair && !mbar_wait_bounded(&sh.q_full[q1], ((qn + 1) >> 1) & 1, abort_flag)))
+          break;
+        const int steps = pair ? 2 * L : L, inc = pair ? 1 : 2;
+        for (int s = -2; s < steps; ++s) {
+          const int i = s & 1;
+          const int l = pair ? s >> 1 : s;
+          const int limit = pair && i == 1 ? L : c0;
+          const bool last = !pair || i == 1;   // the last to read this K, this V
+          if (s >= 0) {
+            if (l < limit) {
+              // O_i (+)= P_i(l) V(l)
+              const bool start = l == (pair ? 0 : i);
+              ok = mbar_wait_bounded(&sh.full[vs], vph, abort_flag);
+              if (l >= fix_l) {
+                const uint32_t k = fb + (l - fix_l);
+                ok = ok && mbar_wait_bounded(&sh.fix_done[k & 1], (k >> 1) & 1, abort_flag);
+              }
+              if (start) {
+                ok = ok && mbar_wait_bounded(&sh.o_empty[i], (no >> i) & 1, abort_flag);
+                no ^= 1u << i;
+              }
+              ok = ok && mbar_wait_bounded(&sh.p_full[i], (np >> i) & 1, abort_flag);
+              if (!ok) break;
+              np ^= 1u << i;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t vd = vd0 + (uint64_t)(vs * (TL::kBytes >> 4));
+#pragma unroll
+                for (int x = 0; x < kKeys / 16; ++x)
+                  umma_bf16_tmem_a(tm + kColO + i * 128, tm + i * kKeys + x * 8,
+                                   vd + (uint64_t)(x * 2 * TL::kGroup >> 4), idesc_o, !start || x > 0);
+                if (last) umma_commit(&sh.empty[vs]);
+                if (l + inc >= limit) umma_commit(&sh.o_full[i]);
+              }
+              __syncwarp();
+            }
+            if (last) advance(vs, vph, 2);
+          }
+          const int ln = l + inc;
+          if (ln < limit) {
+            // S_i(ln) = Q_i K(ln)^T, over the P that the PV before it has read
+            if (!mbar_wait_bounded(&sh.full[ks], kph, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t qd = qd0 + (uint64_t)((i == 0 ? q0 : q1) * (TL::kQBytes >> 4));
+              const uint64_t kd = kd0 + (uint64_t)(ks * (TL::kBytes >> 4));
+#pragma unroll
+              for (int x = 0; x < DH / 16; ++x)
+                umma_bf16(tm + i * kKeys, qd + (uint64_t)(((x >> 2) * TL::kQHalf + (x & 3) * 32) >> 4),
+                          kd + (uint64_t)(((x >> 2) * 1024 + (x & 3) * 32) >> 4), idesc_s, x > 0);
+              umma_commit(&sh.s_full[i]);
+              if (last) umma_commit(&sh.empty[ks]);
+              if (ln == limit - 1) umma_commit(&sh.q_empty[i == 0 ? q0 : q1]);
+              // the V check may wait for V(ln): the entry before it in its slot is behind us
+              if (ln >= fix_l && (!pair || i == (ln < c0 ? 0 : 1)))
+                mbar_arrive(&sh.fix_req[(fb + (ln - fix_l)) & 1]);
+              if (n == 0 && s == -2) DLM_TRACE_MARK(3);
+            }
+            __syncwarp();
+          }
+          if (last && ln < L) advance(ks, kph, 2);
+        }
+        // a row tile without keys here never used its Q
+        if (ok && pair && c0 == 0 && elect_one()) umma_commit(&sh.q_empty[q0]);
+        qn += pair ? 2 : 1;
+        fb += max(0, L - fix_l);
       }
+      __syncwarp();
+      if (elect_one()) umma_commit(&sh.fin);   // every MMA issued has finished
+      mbar_wait_bounded(&sh.fin, 0, nullptr);
     } else if (warp == kScheduler) {
       // ---------------- scheduler: the range's items, one descriptor each ----------------
       const int g1 = sh.stop[0], b_end = sh.stop[1], j_end = sh.stop[2], t_end = sh.stop[3];
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.te = stops ? t_end : kt;
           it.whole = it.ts == 0 && it.te == kt;
           it.slot = it.ts == 0;
-          it.fix0 = visible(it.pos0, ctx, p.block) / kKeys;
+          it.fix = visible(it.pos0, ctx, p.block);
           it.valid = 1;
           const bool empty_cut = !it.whole && it.ts >= it.te;   // nothing of a cut item
           if (!it.whole) {
@@ -639,8 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ---------------- V check of tiles with hidden keys ----------------
       // A hidden key has probability 0, but 0 x infinity is NaN: rows behind the
-      // sequence become zero, and so do non-finite elements (the epilogue adds
-      // them to the rows that see them).
+      // sequence become zero, and so do non-finite elements of keys that only some
+      // rows see (the epilogue adds them to the rows that do).
       uint32_t eb = 0, done = 0;
       bool ok = true;
       for (uint32_t n = 0; ok; ++n) {
@@ -648,45 +652,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_bounded(&sh.d_full[ds], (n / kDescs) & 1, abort_flag)) break;
         Item& it = sh.item[ds];
         if (!it.valid) break;
-        const int ts = it.ts, te = it.te, ctx = it.ctx;
-        for (int t = max(ts, it.fix0); t < te; ++t) {
-          if (!mbar_wait_bounded(&sh.fix_req, done & 1, abort_flag)) {
+        const int ts = it.ts, te = it.te, ctx = it.ctx, fix = it.fix;
+        for (int t = max(ts, fix / kKeys); t < te; ++t) {
+          const uint32_t en = eb + 2 * (t - ts) + 1;
+          if (!mbar_wait_bounded(&sh.fix_req[done & 1], (done >> 1) & 1, abort_flag) ||
+              !mbar_wait_bounded(&sh.full[en % NS], (en / NS) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          const uint32_t en = eb + 2 * (t - ts) + 1;
-          mbar_wait_bounded(&sh.full[en % NS], (en / NS) & 1, abort_flag);   // complete already
           uint8_t* tile = ring + (en % NS) * TL::kBytes;
-          const int live = ctx - t * kKeys;   // rows of the tile that hold tokens
-          bool bad = false;
-          // 16 bytes at a time; rows are 128 bytes, kHalves per 8-row group
-#pragma unroll 8
-          for (int x = lane; x < TL::kBytes / 16; x += 32) {
-            const int r = (x * 16 / TL::kGroup) * 8 + ((x >> 3) & 7);
-            uint4* at = reinterpret_cast<uint4*>(tile + x * 16);
-            if (r >= live) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else {
-              uint4 w = *at;
+          const int live = min(kKeys, ctx - t * kKeys);   // rows that hold tokens
+          // 16-byte pieces: lane / kPieces = row of the group's step, lane % kPieces = piece
+          constexpr int kPieces = TL::kHalves * 8, kStep = 32 / kPieces;
+          const int piece = lane % kPieces, r0 = lane / kPieces;
+          auto at = [&](int r) {
+            return reinterpret_cast<uint4*>(tile + (r >> 3) * TL::kGroup + (piece >> 3) * 1024 +
+                                            (r & 7) * 128 + (piece & 7) * 16);
+          };
+          for (int r = live + r0; r < kKeys; r += kStep) *at(r) = make_uint4(0, 0, 0, 0);
+          // exponent bits all ones: the carry reaches the sign bit
+          auto hot = [](uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; };
+          uint32_t acc = 0;
+          const int first = max(0, fix - t * kKeys) + r0;
+#pragma unroll 4
+          for (int r = first; r < live; r += kStep) {
+            const uint4 w = *at(r);
+            acc |= hot(w.x) | hot(w.y) | hot(w.z) | hot(w.w);
+          }
+          if (__any_sync(0xffffffffu, (acc & 0x80008000u) != 0)) {
+            for (int r = first; r < live; r += kStep) {
+              uint4 w = *at(r);
               uint32_t* c = &w.x;
-              bool hit = false;
 #pragma unroll
-              for (int y = 0; y < 4; ++y) hit |= nonfinite2(c[y]);
-              if (hit) {
-                bad = true;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  if ((c[y] & 0x7F800000u) == 0x7F800000u) c[y] &= 0x0000FFFFu;
-                  if ((c[y] & 0x7F80u) == 0x7F80u) c[y] &= 0xFFFF0000u;
-                }
-                *at = w;
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t h = hot(c[y]);
+                c[y] &= (h & 0x80000000u ? 0u : 0xFFFF0000u) | (h & 0x8000u ? 0u : 0xFFFFu);
               }
+              *at(r) = w;
             }
+            if (lane == 0) it.poison = 1;
           }
           fence_proxy_async_smem();
-          if (__any_sync(0xffffffffu, bad) && lane == 0) it.poison = 1;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.fix_done);
+          if (lane == 0) mbar_arrive(&sh.fix_done[done & 1]);
           ++done;
         }
         eb += 2 * (te - ts);
@@ -730,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        if (ns == 0 && tid == 0) DLM_TRACE_MARK(4);
         tc_fence_after();
         if (any) {   // warps without rows leave their lanes of P as they are
           float sv[kKeys];
@@ -786,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[i]);
+        if (ns == 0 && tid == 0) DLM_TRACE_MARK(5);
       }
       if (!ok) break;
       // ---- epilogue ----
@@ -815,6 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run = l_run * w0 + x.y * w1;
           m_run = mm;
         }
+        if (n == 0 && tid == 0) DLM_TRACE_MARK(6);
         tc_fence_after();
         const bool poison = it.poison != 0;
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
@@ -842,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float x[32];
 #pragma unroll
               for (int z = 0; z < 32; ++z) x[z] = o[z];
-              add_poison<DH>(p, it, max(it.ts, it.fix0) * kKeys, min(lim, it.te * kKeys), y * 32, x);
+              add_poison<DH>(p, it, max(it.ts * kKeys, it.fix), min(lim, it.te * kKeys), y * 32, x);
 #pragma unroll
               for (int z = 0; z < 32; ++z) o[z] = x[z];
             }
@@ -886,6 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (tid == 0) DLM_TRACE_MARK(7);
   tc_fence_before();
   __syncthreads();
   if (warp == kMma) {
@@ -901,6 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int DH>
 __global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_ctas) {
   constexpr int E = DH / 32;
+  DLM_TRACE_CTA(TRACE_PAGED_JOIN);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Meta me = p.meta[c];
