@@ -20,6 +20,8 @@
 // one stride between 8-row groups, which is what the MMA descriptors need.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 
 namespace dlm {
@@ -30,8 +32,11 @@ namespace {
 
 constexpr int kKeys = 128;       // keys per tile
 constexpr int kRows = 128;       // rows per row tile
-constexpr int kThreads = 384;    // 12 warps: softmax 0-3 and 4-7, producer, MMA, scheduler, V check
-constexpr int kProducer = 8, kMma = 9, kScheduler = 10, kFixer = 11;
+// 16 warps: softmax of row tile 0 and 1 (four each), producer, MMA issuers of
+// row tile 0 and 1, scheduler, and four that write results (and check V), so
+// that the softmax goes on with the next item meanwhile
+constexpr int kThreads = 512;
+constexpr int kProducer = 8, kMma = 9, kScheduler = 11, kWriter = 12;
 constexpr int kDescs = 4;
 constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P over S), O0, O1 (Dh each)
 constexpr uint32_t kColO = 256;
@@ -42,9 +47,6 @@ constexpr int kMinKeys = 256;
 // the running reference of a row moves only when its maximum passes it by
 // more than this (log2 units): P stays below 2^8, O is rarely rescaled
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kRegsSoftmax = 224, kRegsOther = 56;
-static_assert(kRegsSoftmax * 256 + kRegsOther * 128 <= 168 * kThreads,
-              "register split exceeds the launch's registers");
 
 template <int DH>
 struct Tile {
@@ -87,11 +89,11 @@ struct Smem {
   static constexpr int kTail = kRing + Tile<DH>::kSlots * Tile<DH>::kBytes;
   struct Rest {
     Item item[kDescs];
-    float2 xml[2][kRows];   // (max, sum) of the second half, alternating between items
+    float2 stat[2][kRows];   // (max, sum) of the rows, per row tile or half
     uint64_t full[Tile<DH>::kSlots], empty[Tile<DH>::kSlots];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2], turn[2][4];
     uint64_t d_full[kDescs], d_empty[kDescs];
-    uint64_t x_full[2], fix_req[2], fix_done[2], fin;
+    uint64_t stat_full[2], stat_empty[2], fix_req[2], fix_done[2], fin[2];
     int start[4], stop[4];
     uint32_t tmem;
     int abort;
@@ -137,6 +139,17 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// Waits of the inner loops: little code (the roles share the instruction
+// caches), bounded by the number of tries, each at most about 2 us long.
+constexpr uint32_t kTries = 1u << 20;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  for (uint32_t n = 0; !mbar_try_wait_hint(bar, parity, 2000u); ++n) {
+    if (n >= kTries) *abort_flag = 1;
+    if (*abort_flag) return false;
+  }
+  return true;
+}
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
   asm volatile(
@@ -147,12 +160,15 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+__device__ __noinline__ int block_end(int p, int ctx, int block) {
+  return (int)min((long long)ctx, ((long long)(p / block) + 1) * block);
+}
 // keys [0, n) that the row at position p sees
 __device__ __forceinline__ int visible(int p, int ctx, int block) {
   if (block == 0) return ctx;
   if (p < 0) return 0;
   if (block == 1) return min(ctx, p + 1);
-  return (int)min((long long)ctx, ((long long)(p / block) + 1) * block);
+  return block_end(p, ctx, block);
 }
 
 // The cost of a sequence's items, in keys: item j (2 * npos positions) costs the
@@ -164,7 +180,7 @@ struct SeqCost {
   bool masked;
   __device__ SeqCost(int n_, int ctx_, int pp_, int block)
       : base((long long)ctx_ - n_), n(n_), ctx(ctx_), pp(pp_), masked(block != 0) {
-    items = (int)(((long long)n + pp - 1) / pp);
+    items = (int)(((uint32_t)n + (uint32_t)pp - 1u) / (uint32_t)pp);
     // items wholly before position 0 (masked, base < 0): no keys
     j0 = base < 0 ? min(max(items - 1, 0), (int)(-base / pp)) : 0;
   }
@@ -191,31 +207,41 @@ __device__ __forceinline__ float fmax3f(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float row_max(const float (&sv)[kKeys]) {
-  float m[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m[k] = fmaxf(sv[k], sv[k + 8]);
-#pragma unroll
-  for (int j = 16; j < kKeys; j += 16)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m[k] = fmax3f(m[k], sv[j + k], sv[j + 8 + k]);
-  return fmax3f(fmax3f(m[0], m[1], m[2]), fmax3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+// two float32 in one register pair (sm_100 packed arithmetic)
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
-// Adds to o (32 columns from c0) the non-finite V elements of keys
-// [k0, k1): the V check set them to zero in shared memory, so that rows that
-// do not see those keys stay clean.
+// Adds to o (16 columns from c0) the non-finite V elements of keys [k0, k1): the
+// V check set them to zero in shared memory, so that rows that do not see
+// those keys stay clean.
 template <int DH>
 __device__ __noinline__ void add_poison(const Params& p, const Item& it, int k0, int k1, int c0,
-                                        float (&o)[32]) {
+                                        float* o) {
   const int mask = (1 << p.page_shift) - 1;
+#pragma unroll 1
   for (int k = k0; k < k1; ++k) {
     const int page = p.table[(size_t)it.b * p.W + (k >> p.page_shift)];
     if (page < 0 || page >= p.n_pages) continue;
     const __nv_bfloat16* row =
         p.v + ((((size_t)page * p.Hkv + it.g) << p.page_shift) + (k & mask)) * DH + c0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {
       const float x = __bfloat162float(row[j]);
       if (!(fabsf(x) <= 3.4e38f)) o[j] += x;
     }
@@ -246,24 +272,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], 2);   // both MMA issuers
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.q_empty[i], 2);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i][0], 4);   // the first 64 keys' P, the others'
+      mbar_init(&sh.p_full[i][1], 4);
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.o_empty[i], 4);
-      mbar_init(&sh.x_full[i], 4);
-      mbar_init(&sh.fix_req[i], 1);
-      mbar_init(&sh.fix_done[i], 1);
+      mbar_init(&sh.stat_full[i], 4);
+      mbar_init(&sh.stat_empty[i], 4);
+      mbar_init(&sh.fix_req[i], 2);
+      mbar_init(&sh.fin[i], 1);
+      mbar_init(&sh.fix_done[i], 4);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&sh.turn[i >> 2][i & 3], 1);
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(&sh.d_full[i], 1);
-      mbar_init(&sh.d_empty[i], 11);   // producer, MMA, V check, 8 softmax warps
+      mbar_init(&sh.d_empty[i], 15);   // all warps but the scheduler
     }
-    mbar_init(&sh.fin, 1);
     sh.abort = 0;
     fence_mbar_init();
     tma_prefetch(&tmK);
@@ -271,12 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch(&tmQ);
   }
   if (warp == kMma) tmem_alloc(&sh.tmem, kTmemCols);
+  // the join may be set up while this grid runs (it waits for the grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this CTA's range of the work ----
   // scan of the sequences' costs (consecutive sequences per thread), then the
   // owners of the range's two ends turn them into (KV head, sequence, item, tile)
   {
-    long long* scan = reinterpret_cast<long long*>(ring);   // [12] warp sums; free until the first load
+    long long* scan = reinterpret_cast<long long*>(ring);   // a sum per warp; free until the first load
     const int pp = 2 * p.npos;
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
@@ -307,11 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const long long first = before + incl - mine;   // cost before sequence b0
     const long long total = w1 * p.Hkv;
-    const long long ctas = max(1ll, min((long long)gridDim.x, total / kMinKeys));
-    auto edge = [&](long long k) {
-      return k >= ctas ? total : (total / ctas) * k + (total % ctas) * k / ctas;
-    };
-    const long long u[2] = {edge(blockIdx.x), edge((long long)blockIdx.x + 1)};
+    // (doubles: every CTA computes the same edges, and no 64-bit divisions)
+    const int ctas = (int)max(1.0, min((double)gridDim.x, floor((double)total * (1.0 / kMinKeys))));
+    const double share = (double)total / ctas;
+    auto edge = [&](int k) { return k >= ctas ? total : min(total, (long long)(share * k)); };
+    const long long u[2] = {edge(blockIdx.x), edge(blockIdx.x + 1)};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       int* dst = e == 0 ? sh.start : sh.stop;
@@ -319,7 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 0) dst[0] = p.Hkv;   // the end
         continue;
       }
-      const int g = (int)(u[e] / w1);
+      int g = (int)((double)u[e] / (double)w1);   // the quotient, or one off it
+      g -= g * w1 > u[e];
+      g += (g + 1) * w1 <= u[e];
       long long r = u[e] - g * w1 - first;
       if (r < 0 || r >= mine) continue;
       for (int b = b0; b < b1; ++b) {
@@ -345,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         dst[0] = g;
         dst[1] = b;
         dst[2] = lo;
-        dst[3] = (int)(at * kt / cost);   // < kt; 0: the item starts in this range
+        // < kt; 0: the item starts in this range
+        dst[3] = max(0, min(kt - 1, (int)((double)at * kt / (double)cost)));
         break;
       }
     }
@@ -358,7 +392,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) DLM_TRACE_MARK(2);
 
   if (warp >= kProducer) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kProducer) {
       // ---------------- producer: Q, K and V tiles ----------------
       uint32_t e = 0;        // ring entries issued (K, V, K, V, ...)
@@ -404,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the item's queries first
             for (int i = 0; i < q_tiles && ok; ++i, ++qn) {
               const int qslot = qn & 1;
-              ok = mbar_wait_bounded(&sh.q_empty[qslot], ((qn >> 1) & 1) ^ 1, abort_flag);
+              ok = wait(&sh.q_empty[qslot], ((qn >> 1) & 1) ^ 1, abort_flag);
               if (ok && lane == 0) {
                 mbar_arrive_expect_tx(&sh.q_full[qslot], (uint32_t)(p.npos * p.G * DH * 2));
                 for (int h = 0; h < TL::kHalves; ++h)
@@ -417,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const int slot = e % NS;
-            if (!mbar_wait_bounded(&sh.empty[slot], ((e / NS) & 1) ^ 1, abort_flag)) {
+            if (!wait(&sh.empty[slot], ((e / NS) & 1) ^ 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -437,31 +470,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t k = qn > 2 ? qn - 2 : 0; k < qn; ++k)
           mbar_wait_bounded(&sh.q_full[k & 1], (k >> 1) & 1, nullptr);
       }
-    } else if (warp == kMma) {
-      // ---------------- MMA issuer ----------------
-      // One fixed order, no polling: with two row tiles PV0(l) S0(l+1) PV1(l)
-      // S1(l+1), with one PV(l) S(l+2) over alternating halves.  While one half's
-      // softmax runs, the tensor core works for the other.  The whole warp walks
-      // the loop and one elected lane issues: operands that are the same in all
-      // lanes reach the MMA without a move per instruction.
+    } else if (warp < kScheduler) {
+      // ---------------- MMA issuers: one warp per row tile (or half) ----------------
+      // In order, per key tile: S_i(l), then P_i(l) V(l).  A wait that follows MMAs
+      // in a warp returns only when those have left its queue, and the tensor core
+      // would run dry meanwhile (measured: 1375 instead of 1025 cycles for 8 + 8
+      // MMAs); with a warp per row tile the other's MMAs fill the gap.  Both warps
+      // wait for, and release, every ring entry: a barrier's phases are then seen
+      // in order whoever uses the entry.  The whole warp walks the loop and one
+      // elected lane issues: operands that are the same in all lanes reach the MMA
+      // without a move per instruction.
+      const int i = warp - kMma;
       constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DH, true);
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t tm_s = __shfl_sync(0xffffffffu, tmem + i * kKeys, 0);
+      const uint32_t tm_o = __shfl_sync(0xffffffffu, tmem + kColO + i * 128, 0);
       const uint64_t kd0 = desc_k(smem_u32(ring), TL::kGroup);
       const uint64_t vd0 = desc_mn(smem_u32(ring), TL::kGroup);
       const uint64_t qd0 = desc_k(smem_u32(qs), 1024);
-      uint32_t ks = 0, kph = 0;      // ring slot and phase of the next S's K
-      uint32_t vs = 1, vph = 0;      // ... of the next P V's V
-      auto advance = [](uint32_t& slot, uint32_t& phase, uint32_t by) {
-        slot += by;
-        if (slot >= NS) {
-          slot -= NS;
+      uint32_t slot = 0, phase = 0;  // ring
+      auto advance = [&]() {
+        if (++slot == NS) {
+          slot = 0;
           phase ^= 1;
         }
       };
       uint32_t qn = 0;               // Q tiles used
-      uint32_t np = 0;               // bit i: phase of the next P of half i
-      uint32_t no = 3;               // bit i: phase of the next wait for an empty O of half i
+      uint32_t np = 0, no = 1;       // phases of the next P, of the next wait for an empty O
       uint32_t fb = 0;               // V checks of earlier items
       bool ok = true;
       for (uint32_t n = 0; ok; ++n) {
@@ -471,86 +506,112 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__shfl_sync(0xffffffffu, it.valid, 0)) break;
         const int L = __shfl_sync(0xffffffffu, it.te - it.ts, 0);
         const bool pair = __shfl_sync(0xffffffffu, it.pair, 0) != 0;
-        const int c0 = pair ? max(0, min(L, __shfl_sync(0xffffffffu, it.kt0 - it.ts, 0))) : L;
+        // own tiles: first, first + step, ... below limit
+        const int first = pair ? 0 : i, step = pair ? 1 : 2;
+        const int limit =
+            pair && i == 0 ? max(0, min(L, __shfl_sync(0xffffffffu, it.kt0 - it.ts, 0))) : L;
         const int fix_l = max(0, __shfl_sync(0xffffffffu, it.fix / kKeys - it.ts, 0));
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.d_empty[ds]);
         if (L == 0) continue;
-        const uint32_t q0 = qn & 1, q1 = pair ? q0 ^ 1 : q0;
-        if (!mbar_wait_bounded(&sh.q_full[q0], (qn >> 1) & 1, abort_flag) ||
-            (pair && !mbar_wait_bounded(&sh.q_full[q1], ((qn + 1) >> 1) & 1, abort_flag)))
+        const uint32_t q0 = qn & 1, qi = pair ? q0 ^ i : q0;
+        if (!wait(&sh.q_full[q0], (qn >> 1) & 1, abort_flag) ||
+            (pair && !wait(&sh.q_full[q0 ^ 1], ((qn + 1) >> 1) & 1, abort_flag)))
           break;
-        const int steps = pair ? 2 * L : L, inc = pair ? 1 : 2;
-        for (int s = -2; s < steps; ++s) {
-          const int i = s & 1;
-          const int l = pair ? s >> 1 : s;
-          const int limit = pair && i == 1 ? L : c0;
-          const bool last = !pair || i == 1;   // the last to read this K, this V
-          if (s >= 0) {
-            if (l < limit) {
-              // O_i (+)= P_i(l) V(l)
-              const bool start = l == (pair ? 0 : i);
-              ok = mbar_wait_bounded(&sh.full[vs], vph, abort_flag);
-              if (l >= fix_l) {
-                const uint32_t k = fb + (l - fix_l);
-                ok = ok && mbar_wait_bounded(&sh.fix_done[k & 1], (k >> 1) & 1, abort_flag);
+        const uint64_t qd = qd0 + (uint64_t)(qi * (TL::kQBytes >> 4));
+        int own = first;   // the next own tile
+        if (own >= limit && lane == 0) {
+          // no tile here (a row tile without keys, a half without a key tile)
+          mbar_arrive(&sh.q_empty[qi]);
+          if (pair) mbar_arrive(&sh.q_empty[qi]);
+        }
+        bool k_there = false;
+        for (int l = 0; l < L; ++l) {
+          const bool mine = l == own && l < limit;
+          const bool last = l + step >= limit;
+          if (!k_there && !wait(&sh.full[slot], phase, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (mine) {
+            // S_i(l) = Q_i K(l)^T, over the P that the P V before it has read
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t kd = kd0 + (uint64_t)(slot * (TL::kBytes >> 4));
+#pragma unroll
+              for (int x = 0; x < DH / 16; ++x)
+                umma_bf16(tm_s, qd + (uint64_t)(((x >> 2) * TL::kQHalf + (x & 3) * 32) >> 4),
+                          kd + (uint64_t)(((x >> 2) * 1024 + (x & 3) * 32) >> 4), idesc_s, x > 0);
+              umma_commit(&sh.s_full[i]);
+              umma_commit(&sh.empty[slot]);
+              if (last) {
+                umma_commit(&sh.q_empty[qi]);
+                if (pair) umma_commit(&sh.q_empty[qi]);   // one for each issuer
               }
-              if (start) {
-                ok = ok && mbar_wait_bounded(&sh.o_empty[i], (no >> i) & 1, abort_flag);
-                no ^= 1u << i;
-              }
-              ok = ok && mbar_wait_bounded(&sh.p_full[i], (np >> i) & 1, abort_flag);
+              if (l == 0 && n == 0) DLM_TRACE_MARK(3);
+            }
+          } else if (lane == 0) {
+            mbar_arrive(&sh.empty[slot]);
+          }
+          // the V check may look at V(l): both issuers are done with what its slot held
+          if (l >= fix_l && lane == 0) mbar_arrive(&sh.fix_req[(fb + (l - fix_l)) & 1]);
+          __syncwarp();
+          advance();
+          if (!wait(&sh.full[slot], phase, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (mine) {
+            // O_i (+)= P_i(l) V(l)
+            if (l >= fix_l) {
+              const uint32_t k = fb + (l - fix_l);
+              ok = wait(&sh.fix_done[k & 1], (k >> 1) & 1, abort_flag);
+            }
+            if (l == first) {
+              ok = ok && wait(&sh.o_empty[i], no, abort_flag);
+              no ^= 1;
+            }
+            // two row tiles: the next K first, so that its S follows at once
+            k_there = pair && !last;
+            if (k_there) {
+              const bool wrap = slot + 1 == NS;
+              ok = ok && wait(&sh.full[wrap ? 0 : slot + 1], phase ^ (wrap ? 1u : 0u), abort_flag);
+            }
+            // in two halves: the first runs during the second's exponentials
+            const uint64_t vd = vd0 + (uint64_t)(slot * (TL::kBytes >> 4));
+#pragma unroll 1
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = wait(&sh.p_full[i][h], np, abort_flag);
               if (!ok) break;
-              np ^= 1u << i;
               tc_fence_after();
               if (elect_one()) {
-                const uint64_t vd = vd0 + (uint64_t)(vs * (TL::kBytes >> 4));
 #pragma unroll
-                for (int x = 0; x < kKeys / 16; ++x)
-                  umma_bf16_tmem_a(tm + kColO + i * 128, tm + i * kKeys + x * 8,
-                                   vd + (uint64_t)(x * 2 * TL::kGroup >> 4), idesc_o, !start || x > 0);
-                if (last) umma_commit(&sh.empty[vs]);
-                if (l + inc >= limit) umma_commit(&sh.o_full[i]);
+                for (int x = 0; x < kKeys / 32; ++x)
+                  umma_bf16_tmem_a(tm_o, tm_s + h * 32 + x * 8,
+                                   vd + (uint64_t)((h * 8 + x * 2) * TL::kGroup >> 4), idesc_o,
+                                   l != first || h > 0 || x > 0);
+                if (h == 1) {
+                  umma_commit(&sh.empty[slot]);
+                  if (last) umma_commit(&sh.o_full[i]);
+                }
               }
               __syncwarp();
             }
-            if (last) advance(vs, vph, 2);
+            np ^= 1;
+            if (!ok) break;
+            own += step;
+          } else if (lane == 0) {
+            mbar_arrive(&sh.empty[slot]);
           }
-          const int ln = l + inc;
-          if (ln < limit) {
-            // S_i(ln) = Q_i K(ln)^T, over the P that the PV before it has read
-            if (!mbar_wait_bounded(&sh.full[ks], kph, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t qd = qd0 + (uint64_t)((i == 0 ? q0 : q1) * (TL::kQBytes >> 4));
-              const uint64_t kd = kd0 + (uint64_t)(ks * (TL::kBytes >> 4));
-#pragma unroll
-              for (int x = 0; x < DH / 16; ++x)
-                umma_bf16(tm + i * kKeys, qd + (uint64_t)(((x >> 2) * TL::kQHalf + (x & 3) * 32) >> 4),
-                          kd + (uint64_t)(((x >> 2) * 1024 + (x & 3) * 32) >> 4), idesc_s, x > 0);
-              umma_commit(&sh.s_full[i]);
-              if (last) umma_commit(&sh.empty[ks]);
-              if (ln == limit - 1) umma_commit(&sh.q_empty[i == 0 ? q0 : q1]);
-              // the V check may wait for V(ln): the entry before it in its slot is behind us
-              if (ln >= fix_l && (!pair || i == (ln < c0 ? 0 : 1)))
-                mbar_arrive(&sh.fix_req[(fb + (ln - fix_l)) & 1]);
-              if (n == 0 && s == -2) DLM_TRACE_MARK(3);
-            }
-            __syncwarp();
-          }
-          if (last && ln < L) advance(ks, kph, 2);
+          __syncwarp();
+          advance();
         }
-        // a row tile without keys here never used its Q
-        if (ok && pair && c0 == 0 && elect_one()) umma_commit(&sh.q_empty[q0]);
         qn += pair ? 2 : 1;
         fb += max(0, L - fix_l);
       }
       __syncwarp();
-      if (elect_one()) umma_commit(&sh.fin);   // every MMA issued has finished
-      mbar_wait_bounded(&sh.fin, 0, nullptr);
+      if (elect_one()) umma_commit(&sh.fin[i]);   // every MMA issued has finished
+      mbar_wait_bounded(&sh.fin[i], 0, nullptr);
     } else if (warp == kScheduler) {
       // ---------------- scheduler: the range's items, one descriptor each ----------------
       const int g1 = sh.stop[0], b_end = sh.stop[1], j_end = sh.stop[2], t_end = sh.stop[3];
@@ -641,46 +702,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       (void)ok;
       if (lane == 0) p.meta[blockIdx.x] = meta;
     } else {
-      // ---------------- V check of tiles with hidden keys ----------------
-      // A hidden key has probability 0, but 0 x infinity is NaN: rows behind the
-      // sequence become zero, and so do non-finite elements of keys that only some
-      // rows see (the epilogue adds them to the rows that do).
+      // ---------------- writers: V check, results ----------------
+      // A hidden key has probability 0, but 0 x infinity is NaN: in tiles with hidden
+      // keys, rows of V behind the sequence become zero, and so do non-finite
+      // elements of keys that only some rows see (added back below to the rows that
+      // do).
+      const int quad = warp - kWriter;
+      const int row = quad * 32 + lane;
+      const uint32_t o_col = tmem + ((uint32_t)(quad * 32) << 16) + kColO;
+      const int rp = row / p.G, rh = row - rp * p.G;   // position and head of the row
       uint32_t eb = 0, done = 0;
-      bool ok = true;
-      for (uint32_t n = 0; ok; ++n) {
+      uint32_t no[2] = {0, 0};                         // O accumulations taken
+      for (uint32_t n = 0;; ++n) {
         const int ds = n % kDescs;
         if (!mbar_wait_bounded(&sh.d_full[ds], (n / kDescs) & 1, abort_flag)) break;
         Item& it = sh.item[ds];
         if (!it.valid) break;
-        const int ts = it.ts, te = it.te, ctx = it.ctx, fix = it.fix;
+        const int ts = it.ts, te = it.te, ctx = it.ctx, fix = it.fix, L = te - ts;
+        const bool pair = it.pair != 0;
+        bool ok = true;
         for (int t = max(ts, fix / kKeys); t < te; ++t) {
           const uint32_t en = eb + 2 * (t - ts) + 1;
-          if (!mbar_wait_bounded(&sh.fix_req[done & 1], (done >> 1) & 1, abort_flag) ||
-              !mbar_wait_bounded(&sh.full[en % NS], (en / NS) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
+          ok = wait(&sh.fix_req[done & 1], (done >> 1) & 1, abort_flag) &&
+               wait(&sh.full[en % NS], (en / NS) & 1, abort_flag);
+          if (!ok) break;
           uint8_t* tile = ring + (en % NS) * TL::kBytes;
           const int live = min(kKeys, ctx - t * kKeys);   // rows that hold tokens
-          // 16-byte pieces: lane / kPieces = row of the group's step, lane % kPieces = piece
+          // 16-byte pieces: a warp takes kStep rows at a time, four warps in turn
           constexpr int kPieces = TL::kHalves * 8, kStep = 32 / kPieces;
-          const int piece = lane % kPieces, r0 = lane / kPieces;
+          const int piece = lane % kPieces, r0 = lane / kPieces + quad * kStep;
           auto at = [&](int r) {
             return reinterpret_cast<uint4*>(tile + (r >> 3) * TL::kGroup + (piece >> 3) * 1024 +
                                             (r & 7) * 128 + (piece & 7) * 16);
           };
-          for (int r = live + r0; r < kKeys; r += kStep) *at(r) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+          for (int r = live + r0; r < kKeys; r += 4 * kStep) *at(r) = make_uint4(0, 0, 0, 0);
           // exponent bits all ones: the carry reaches the sign bit
           auto hot = [](uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; };
           uint32_t acc = 0;
           const int first = max(0, fix - t * kKeys) + r0;
 #pragma unroll 4
-          for (int r = first; r < live; r += kStep) {
+          for (int r = first; r < live; r += 4 * kStep) {
             const uint4 w = *at(r);
             acc |= hot(w.x) | hot(w.y) | hot(w.z) | hot(w.w);
           }
           if (__any_sync(0xffffffffu, (acc & 0x80008000u) != 0)) {
-            for (int r = first; r < live; r += kStep) {
+#pragma unroll 1
+            for (int r = first; r < live; r += 4 * kStep) {
               uint4 w = *at(r);
               uint32_t* c = &w.x;
 #pragma unroll
@@ -697,24 +765,120 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&sh.fix_done[done & 1]);
           ++done;
         }
-        eb += 2 * (te - ts);
-        __syncwarp();
+        if (!ok) break;
+        eb += 2 * L;
+        // ---- results: row tile 0, then 1; of one tile, the two halves together ----
+        const int c0 = pair ? max(0, min(L, it.kt0 - ts)) : (L + 1) >> 1;
+        const int c1 = pair ? L : L >> 1;
+        const int tiles = pair ? 2 : 1;
+        for (int i = 0; i < tiles; ++i) {
+          const int c = i == 0 ? c0 : c1;
+          const bool two = !pair && c1 > 0;
+          ok = wait(&sh.stat_full[i], n & 1, abort_flag) &&
+               (pair || wait(&sh.stat_full[1], n & 1, abort_flag)) &&
+               (c == 0 || wait(&sh.o_full[i], no[i] & 1, abort_flag)) &&
+               (!two || wait(&sh.o_full[1], no[1] & 1, abort_flag));
+          if (!ok) break;
+          const int pos = pair ? i * p.npos + rp : rp;
+          const bool live = rp < p.npos && pos < it.npos;
+          const bool whole = it.whole != 0, poison = it.poison != 0;
+          float m = sh.stat[i][row].x, l = sh.stat[i][row].y;
+          float w0 = 1.f, w1 = 0.f;
+          if (two) {
+            const float2 x = sh.stat[1][row];
+            const float mm = fmaxf(m, x.x);
+            w0 = m == -CUDART_INF_F ? 0.f : fast_exp2(m - mm);
+            w1 = x.x == -CUDART_INF_F ? 0.f : fast_exp2(x.x - mm);
+            l = l * w0 + x.y * w1;
+            m = mm;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.stat_empty[i]);
+            if (!pair) mbar_arrive(&sh.stat_empty[1]);
+          }
+          tc_fence_after();
+          if (n == 0 && quad == 0 && lane == 0) DLM_TRACE_MARK(6);
+          if (whole) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            w0 *= inv;
+            w1 *= inv;
+          }
+          const size_t prow =
+              ((size_t)blockIdx.x * 2 + it.slot) * (2 * kRows) + (pair ? i * kRows : 0) + row;
+          const int64_t grow = (int64_t)it.row0 + pos;
+          const int head = it.g * p.G + rh;
+          if (__any_sync(0xffffffffu, live)) {
+            uint4* dst_o = reinterpret_cast<uint4*>(p.o + grow * p.o_stride + (int64_t)head * DH);
+            float4* dst_p = reinterpret_cast<float4*>(p.part + prow * DH);
+            // 16 columns at a time: little code, which runs once per item
+#pragma unroll 1
+            for (int y = 0; y < DH / 16; ++y) {
+              float o[16];
+              {
+                uint32_t r0[16], r1[16];
+                tmem_ld16_nowait(o_col + i * 128 + y * 16, r0);
+                if (two) tmem_ld16_nowait(o_col + 128 + y * 16, r1);
+                tmem_wait_ld();
+                // c == 0: no key was seen, and O holds an earlier item's
+#pragma unroll
+                for (int z = 0; z < 16; ++z) o[z] = c > 0 ? __uint_as_float(r0[z]) * w0 : 0.f;
+                if (two)
+#pragma unroll
+                  for (int z = 0; z < 16; ++z) o[z] = fmaf(__uint_as_float(r1[z]), w1, o[z]);
+              }
+              if (poison && live) {
+                const int lim = visible(it.pos0 + pos, ctx, p.block);
+                float x[16];
+#pragma unroll
+                for (int z = 0; z < 16; ++z) x[z] = o[z];
+                add_poison<DH>(p, it, max(ts * kKeys, fix), min(lim, te * kKeys), y * 16, x);
+#pragma unroll
+                for (int z = 0; z < 16; ++z) o[z] = x[z];
+              }
+              if (live && whole) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                  dst_o[y * 2 + z] =
+                      make_uint4(pack_bf16(o[8 * z], o[8 * z + 1]), pack_bf16(o[8 * z + 2], o[8 * z + 3]),
+                                 pack_bf16(o[8 * z + 4], o[8 * z + 5]), pack_bf16(o[8 * z + 6], o[8 * z + 7]));
+              } else if (live) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                  dst_p[y * 4 + z] = make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+              }
+            }
+            if (live && !whole)
+              p.ml[prow] = make_float2(m, l);
+            else if (live && p.lse != nullptr)
+              p.lse[(size_t)grow * p.H + head] =
+                  l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (c > 0) mbar_arrive(&sh.o_empty[i]);
+            if (two) mbar_arrive(&sh.o_empty[1]);
+          }
+        }
+        if (!ok) break;
+        no[0] += c0 > 0;
+        no[1] += c1 > 0;
         if (lane == 0) mbar_arrive(&sh.d_empty[ds]);
       }
+      if (quad == 0 && lane == 0) DLM_TRACE_MARK(7);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    // ---------------- softmax and epilogue: one row per thread ----------------
+    // ---------------- softmax: one row per thread ----------------
     const int i = warp >> 2;                          // row tile
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t s_col = lane_addr + i * kKeys;
-    const uint32_t o_col = lane_addr + kColO;
-    const int rp = row / p.G, rh = row - rp * p.G;    // position and head of the row
+    const uint32_t o_col = lane_addr + kColO + i * 128;
+    const int rp = row / p.G;                     // position of the row
     uint32_t ns = 0;                                  // S tiles taken
-    uint32_t no[2] = {0, 0};                          // O accumulations finished
-    uint32_t nx = 0;                                  // exchanges of (max, sum)
+    uint32_t nt = 0;                                  // phase of the next turn
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
       const int ds = n % kDescs;
@@ -731,173 +895,148 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = live ? visible(it.pos0 + pos, it.ctx, p.block) : 0x7fffffff;
       const int lim_min = __reduce_min_sync(0xffffffffu, lim);
       const bool any = __any_sync(0xffffffffu, live);
+      // The two row tiles (halves) take turns at the exponentials, each warp with
+      // the one that shares its scheduler.  Left alone they fall into step, both
+      // at the exponential unit and then both at the tensor core (prompts case:
+      // 1437 us against 1291 in turns).
+      const int turns = min(c0, c1);
+      auto take_turn = [&](int x) {
+        if (x >= turns) return true;
+        const bool mine = wait(&sh.turn[i][quad], nt ^ (i == 0 ? 1u : 0u), abort_flag);
+        nt ^= 1;
+        return mine;
+      };
+      auto pass_turn = [&](int x) {
+        if (x < turns && lane == 0) mbar_arrive(&sh.turn[i ^ 1][quad]);
+      };
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int x = 0; x < c; ++x, ++ns) {
         const int t = it.ts + (pair ? x : 2 * x + i);
-        if (!mbar_wait_bounded(&sh.s_full[i], ns & 1, abort_flag)) {
+        if (!wait(&sh.s_full[i], ns & 1, abort_flag)) {
           ok = false;
           break;
         }
         if (ns == 0 && tid == 0) DLM_TRACE_MARK(4);
         tc_fence_after();
         if (any) {   // warps without rows leave their lanes of P as they are
-          float sv[kKeys];
-          {
-            uint32_t raw[kKeys / 32][32];
-#pragma unroll
-            for (int y = 0; y < kKeys / 32; ++y) tmem_ld32_nowait(s_col + y * 32, raw[y]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int y = 0; y < kKeys / 32; ++y)
-#pragma unroll
-              for (int z = 0; z < 32; ++z) sv[y * 32 + z] = __uint_as_float(raw[y][z]);
-          }
           const int left = lim - t * kKeys;
           if (lim_min - t * kKeys < kKeys) {
+            // hidden keys: their scores become -inf in tensor memory (few tiles, so
+            // the loops below need no mask)
+#pragma unroll 1
+            for (int y = 0; y < kKeys / 32; ++y) {
+              uint32_t raw[32];
+              tmem_ld32_nowait(s_col + y * 32, raw);
+              tmem_wait_ld();
 #pragma unroll
-            for (int z = 0; z < kKeys; ++z)
-              if (z >= left) sv[z] = -CUDART_INF_F;
+              for (int z = 0; z < 32; ++z)
+                if (y * 32 + z >= left) raw[z] = 0xff800000u;
+              tmem_st32_u(s_col + y * 32, raw);
+            }
+            tmem_wait_st();
           }
-          const float mx = row_max(sv) * p.scale_log2;
+          // The scores are read twice, for the maximum and for the exponentials,
+          // in loops of 32 columns: unrolled over 128 columns in registers the code
+          // fell out of the instruction caches, which held up the MMA warp
+          float mx = -CUDART_INF_F;
+#pragma unroll 1
+          for (int y = 0; y < kKeys / 64; ++y) {
+            uint32_t r0[32], r1[32];
+            tmem_ld32_nowait(s_col + y * 64, r0);
+            tmem_ld32_nowait(s_col + y * 64 + 32, r1);
+            tmem_wait_ld();
+            float m4[4] = {mx, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int z = 0; z < 32; ++z)
+              m4[z & 3] = fmax3f(m4[z & 3], __uint_as_float(r0[z]), __uint_as_float(r1[z]));
+            mx = fmax3f(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+          }
+          mx *= p.scale_log2;
           const bool move = __any_sync(0xffffffffu, mx > m_run + kRescaleLog2);
           const float m_new = move ? fmaxf(m_run, mx) : m_run;
           const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // no key seen yet
           const float alpha = move ? fast_exp2(m_run - base) : 1.f;
-          float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int y = 0; y < kKeys / 32; ++y) {
-            uint32_t w[16];
-#pragma unroll
-            for (int z = 0; z < 16; ++z) {
-              const float e0 = fast_exp2(fmaf(sv[32 * y + 2 * z], p.scale_log2, -base));
-              const float e1 = fast_exp2(fmaf(sv[32 * y + 2 * z + 1], p.scale_log2, -base));
-              rs[z & 7] += e0 + e1;
-              w[z] = pack_bf16(e0, e1);   // the MMA's operand type; the sum keeps float32
-            }
-            tmem_st16_u(s_col + y * 16, w);
-          }
-          l_run = l_run * alpha +
-                  (((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7])));
-          m_run = m_new;
           // S(x) was issued after P(x-1) V, so O holds every earlier tile
           if (x > 0 && move) {
 #pragma unroll 1
             for (int y = 0; y < DH / 32; ++y) {
               float o[32];
-              tmem_ld32(o_col + i * 128 + y * 32, o);
+              tmem_ld32(o_col + y * 32, o);
 #pragma unroll
               for (int z = 0; z < 32; ++z) o[z] *= alpha;
-              tmem_st32(o_col + i * 128 + y * 32, o);
+              tmem_st32(o_col + y * 32, o);
             }
           }
-          tmem_wait_st();
+          const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(-base, -base);
+          uint64_t rs[2] = {0, 0};
+          // P in the MMA's operand type, two keys a column, over columns of S that
+          // have been read; the sum keeps float32
+          auto exp32 = [&](const uint32_t (&raw)[32], int y) {
+            uint32_t w[16];
+#pragma unroll
+            for (int z = 0; z < 16; ++z) {
+              float e0, e1;
+              const uint64_t x = fma2(
+                  pack2(__uint_as_float(raw[2 * z]), __uint_as_float(raw[2 * z + 1])), scale2, base2);
+              unpack2(x, e0, e1);
+              e0 = fast_exp2(e0);
+              e1 = fast_exp2(e1);
+              rs[z & 1] = add2(rs[z & 1], pack2(e0, e1));
+              w[z] = pack_bf16(e0, e1);
+            }
+            tmem_st16_u(s_col + y * 16, w);
+          };
+          uint32_t ra[32], rb[32];
+          if (!take_turn(x)) {
+            ok = false;
+            break;
+          }
+          tmem_ld32_nowait(s_col, ra);
+#pragma unroll 1
+          for (int y = 0; y < kKeys / 32; y += 2) {
+            tmem_wait_ld();
+            tmem_ld32_nowait(s_col + y * 32 + 32, rb);
+            exp32(ra, y);
+            tmem_wait_ld();
+            if (y + 2 < kKeys / 32) tmem_ld32_nowait(s_col + y * 32 + 64, ra);
+            exp32(rb, y + 1);
+            // P V of these 64 keys may start
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[i][y >> 1]);
+          }
+          pass_turn(x);
+          {
+            float s0, s1;
+            unpack2(add2(rs[0], rs[1]), s0, s1);
+            l_run = l_run * alpha + (s0 + s1);
+          }
+          m_run = m_new;
+        } else {
+          if (!take_turn(x)) {
+            ok = false;
+            break;
+          }
+          pass_turn(x);
+          tc_fence_before();
+          __syncwarp();
+          if (lane < 2) mbar_arrive(&sh.p_full[i][lane]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[i]);
         if (ns == 0 && tid == 0) DLM_TRACE_MARK(5);
       }
       if (!ok) break;
-      // ---- epilogue ----
-      const int nr = pair ? i * kRows + row : row;   // row of the item
-      if (!pair && c1 > 0) {
-        if (i == 1) {
-          // two buffers: this half can be one item ahead of the other's
-          // epilogue, not two (its P V waits for o_empty)
-          sh.xml[nx & 1][row] = make_float2(m_run, l_run);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.x_full[nx & 1]);
-        } else if (!mbar_wait_bounded(&sh.x_full[nx & 1], (nx >> 1) & 1, abort_flag)) {
-          break;
-        }
-        ++nx;
-      }
-      if (pair || i == 0) {
-        float w0 = 1.f, w1 = 0.f;
-        const bool two = !pair && c1 > 0;
-        if (c > 0 && !mbar_wait_bounded(&sh.o_full[i], no[i] & 1, abort_flag)) break;
-        if (two) {
-          if (!mbar_wait_bounded(&sh.o_full[1], no[1] & 1, abort_flag)) break;
-          const float2 x = sh.xml[(nx & 1) ^ 1][row];
-          const float mm = fmaxf(m_run, x.x);
-          w0 = m_run == -CUDART_INF_F ? 0.f : fast_exp2(m_run - mm);
-          w1 = x.x == -CUDART_INF_F ? 0.f : fast_exp2(x.x - mm);
-          l_run = l_run * w0 + x.y * w1;
-          m_run = mm;
-        }
-        if (n == 0 && tid == 0) DLM_TRACE_MARK(6);
-        tc_fence_after();
-        const bool poison = it.poison != 0;
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-        const size_t prow = ((size_t)blockIdx.x * 2 + it.slot) * (2 * kRows) + nr;
-        const int64_t grow = (int64_t)it.row0 + pos;
-        const int head = it.g * p.G + rh;
-        if (any) {
-#pragma unroll 1
-          for (int y = 0; y < DH / 32; ++y) {
-            float o[32];
-            if (c > 0) {
-              tmem_ld32(o_col + i * 128 + y * 32, o);
-            } else {
-#pragma unroll
-              for (int z = 0; z < 32; ++z) o[z] = 0.f;
-            }
-            if (two) {
-              float o1[32];
-              tmem_ld32(o_col + 128 + y * 32, o1);
-#pragma unroll
-              for (int z = 0; z < 32; ++z) o[z] = o[z] * w0 + o1[z] * w1;
-            }
-            if (!live) continue;
-            if (poison) {
-              float x[32];
-#pragma unroll
-              for (int z = 0; z < 32; ++z) x[z] = o[z];
-              add_poison<DH>(p, it, max(it.ts * kKeys, it.fix), min(lim, it.te * kKeys), y * 32, x);
-#pragma unroll
-              for (int z = 0; z < 32; ++z) o[z] = x[z];
-            }
-            if (it.whole) {
-              uint4* dst = reinterpret_cast<uint4*>(p.o + grow * p.o_stride + (int64_t)head * DH + y * 32);
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                uint4 w;
-                w.x = pack_bf16(o[8 * z] * inv, o[8 * z + 1] * inv);
-                w.y = pack_bf16(o[8 * z + 2] * inv, o[8 * z + 3] * inv);
-                w.z = pack_bf16(o[8 * z + 4] * inv, o[8 * z + 5] * inv);
-                w.w = pack_bf16(o[8 * z + 6] * inv, o[8 * z + 7] * inv);
-                dst[z] = w;
-              }
-            } else {
-              float4* dst = reinterpret_cast<float4*>(p.part + prow * DH + y * 32);
-#pragma unroll
-              for (int z = 0; z < 8; ++z)
-                dst[z] = make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
-            }
-          }
-          if (live) {
-            if (!it.whole)
-              p.ml[prow] = make_float2(m_run, l_run);
-            else if (p.lse != nullptr)
-              p.lse[(size_t)grow * p.H + head] =
-                  l_run == 0.f ? -CUDART_INF_F : (m_run + log2f(l_run)) * 0.69314718055994531f;
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (c > 0) mbar_arrive(&sh.o_empty[i]);
-          if (two) mbar_arrive(&sh.o_empty[1]);
-        }
-      }
-      no[0] += c0 > 0;
-      no[1] += c1 > 0;
+      // the rows' maximum and sum for the writers
+      if (!wait(&sh.stat_empty[i], (n & 1) ^ 1, abort_flag)) break;
+      sh.stat[i][row] = make_float2(m_run, l_run);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.d_empty[ds]);
+      if (lane == 0) {
+        mbar_arrive(&sh.stat_full[i]);
+        mbar_arrive(&sh.d_empty[ds]);
+      }
     }
   }
 
-  if (tid == 0) DLM_TRACE_MARK(7);
   tc_fence_before();
   __syncthreads();
   if (warp == kMma) {
@@ -908,62 +1047,109 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partials of an item that starts in CTA c: c's own, then those of
-// c + 1, ... up to the CTA where it ends, in that order.  One warp per row,
-// lane = DH / 32 columns.
+// c + 1, ... up to the CTA where it ends, in that order.  A warp joins
+// kJoinWarpRows rows at once, lane = DH / 32 columns: the partials' maxima and
+// sums 32 at a time in the lanes, then their rows in batches of independent
+// loads (the join is a chain of loads, so it is the number of links that counts).
+constexpr int kJoinWarpRows = 4, kJoinRows = 8 * kJoinWarpRows;
 template <int DH>
 __global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_ctas) {
-  constexpr int E = DH / 32;
+  constexpr int E = DH / 32, R = kJoinWarpRows;
+  using Vec = typename std::conditional<E == 4, float4, float2>::type;
   DLM_TRACE_CTA(TRACE_PAGED_JOIN);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Meta me = p.meta[c];
-  if (!me.tail) return;
-  const int rows = me.pair ? 2 * kRows : kRows;
-  if ((int)blockIdx.y * 32 >= rows) return;
-  // the CTA where the item ends
-  int last = c;
-  for (int k0 = c + 1; k0 < n_ctas; k0 += 32) {
+  // rows r0 + 8 u of row tile `tile`; those in use are the tile's first ones
+  const int tile = blockIdx.y * kJoinRows / kRows;
+  const int r0 = blockIdx.y * kJoinRows + warp;
+  const int used = tile * kRows + min(p.npos, me.npos - tile * p.npos) * p.G;
+  if (!me.tail || r0 >= used) return;
+  float m[R], l[R], acc[R][E];
+#pragma unroll
+  for (int u = 0; u < R; ++u) {
+    m[u] = -CUDART_INF_F;
+    l[u] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[u][e] = 0.f;
+  }
+  bool ends = false;
+  for (int k0 = c; k0 < n_ctas && !ends; k0 += 32) {
     const int k = k0 + lane;
-    const bool ends = k < n_ctas && p.meta[k].head_ends != 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, ends);
-    if (m != 0) {
-      last = k0 + __ffs(m) - 1;
-      break;
+    const bool next = k < n_ctas && k > c;
+    const bool here = k == c || (next && p.meta[k].head != 0);
+    const uint32_t stops = __ballot_sync(0xffffffffu, next && p.meta[k].head_ends != 0);
+    ends = stops != 0;
+    const int n = ends ? __ffs(stops) : min(32, n_ctas - k0);   // partials of this batch
+    float w[R];
+    {
+      float2 v[R];
+#pragma unroll
+      for (int u = 0; u < R; ++u)
+        v[u] = here && lane < n && r0 + 8 * u < used ? p.ml[((size_t)k * 2 + (k == c)) * (2 * kRows) + r0 + 8 * u]
+                                : make_float2(-CUDART_INF_F, 0.f);
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        float bm = v[u].x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
+        const float m_new = fmaxf(m[u], bm);
+        const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // no key seen so far
+        const float old = fast_exp2(m[u] - base);
+        w[u] = fast_exp2(v[u].x - base);
+        float bl = w[u] == 0.f ? 0.f : w[u] * v[u].y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) bl += __shfl_xor_sync(0xffffffffu, bl, d);
+        l[u] = l[u] * old + bl;
+        m[u] = m_new;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[u][e] *= old;
+      }
+    }
+    constexpr int kB = 4;
+    for (int s = 0; s < n; s += kB) {
+      Vec y[R][kB];
+      float ws[R][kB];
+#pragma unroll
+      for (int x = 0; x < kB; ++x) {
+        const size_t row =
+            ((size_t)(k0 + s + x) * 2 + (k0 + s + x == c)) * (2 * kRows) + r0;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          ws[u][x] = __shfl_sync(0xffffffffu, w[u], (s + x) & 31);
+          if (s + x >= n) ws[u][x] = 0.f;
+          // (a weight of 0: no partial, or rows behind the item's last)
+          if (ws[u][x] != 0.f)
+            y[u][x] = *reinterpret_cast<const Vec*>(p.part + (row + 8 * u) * DH + lane * E);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kB; ++x)
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+          if (ws[u][x] != 0.f) {
+            const float* f = reinterpret_cast<const float*>(&y[u][x]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[u][e] = fmaf(ws[u][x], f[e], acc[u][e]);
+          }
     }
   }
-  for (int r = blockIdx.y * 32 + warp; r < min(rows, (int)blockIdx.y * 32 + 32); r += 8) {
-    const int tile = r / kRows, x = r - tile * kRows;
+#pragma unroll
+  for (int u = 0; u < R; ++u) {
+    if (r0 + 8 * u >= used) continue;
+    const int x = r0 + 8 * u - tile * kRows;
     const int rp = x / p.G, rh = x - rp * p.G, pos = tile * p.npos + rp;
-    if (rp >= p.npos || pos >= me.npos) continue;
-    float m = -CUDART_INF_F;
-    for (int k = c + lane; k <= last; k += 32)
-      if (k == c || p.meta[k].head) m = fmaxf(m, p.ml[((size_t)k * 2 + (k == c)) * (2 * kRows) + r].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float l = 0.f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int k = c; k <= last; ++k) {
-      if (k != c && !p.meta[k].head) continue;
-      const size_t at = ((size_t)k * 2 + (k == c)) * (2 * kRows) + r;
-      const float2 v = p.ml[at];
-      if (v.x == -CUDART_INF_F) continue;
-      const float w = fast_exp2(v.x - m);
-      l += v.y * w;
-      if (w == 0.f) continue;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += w * p.part[at * DH + lane * E + e];
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
     const int64_t grow = (int64_t)me.row0 + pos;
     const int head = me.g * p.G + rh;
     __nv_bfloat16* dst = p.o + grow * p.o_stride + (int64_t)head * DH + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+      *reinterpret_cast<__nv_bfloat162*>(dst + e) =
+          __floats2bfloat162_rn(acc[u][e] * inv, acc[u][e + 1] * inv);
     if (p.lse != nullptr && lane == 0)
       p.lse[(size_t)grow * p.H + head] =
-          l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+          l[u] == 0.f ? -CUDART_INF_F : (m[u] + log2f(l[u])) * 0.69314718055994531f;
   }
 }
 
@@ -1031,7 +1217,7 @@ cudaError_t launch(const PagedAttn& a, int num_sms, cudaStream_t st) {
     return cudaErrorInvalidValue;
   paged_attn_kernel<DH><<<num_sms, kThreads, Smem<DH>::kBytes, st>>>(tmK, tmV, tmQ, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_pdl(paged_join_kernel<DH>, dim3(num_sms, 2 * kRows / 32), dim3(256), 0, st, p, num_sms);
+  return launch_pdl(paged_join_kernel<DH>, dim3(num_sms, 2 * kRows / kJoinRows), dim3(256), 0, st, p, num_sms);
 }
 
 }  // namespace
