@@ -525,7 +525,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh.q_empty[qi]);
           if (pair) mbar_arrive(&sh.q_empty[qi]);
         }
-        bool k_there = false;
+        // S_i(l) = Q_i K(l)^T, over the P that the P V before it has read
+        auto issue_s = [&](uint32_t ks) {
+          const uint64_t kd = kd0 + (uint64_t)(ks * (TL::kBytes >> 4));
+#pragma unroll
+          for (int x = 0; x < DH / 16; ++x)
+            umma_bf16(tm_s, qd + (uint64_t)(((x >> 2) * TL::kQHalf + (x & 3) * 32) >> 4),
+                      kd + (uint64_t)(((x >> 2) * 1024 + (x & 3) * 32) >> 4), idesc_s, x > 0);
+        };
+        auto release_q = [&]() {
+          umma_commit(&sh.q_empty[qi]);
+          if (pair) umma_commit(&sh.q_empty[qi]);   // one for each issuer
+        };
+        bool k_there = false;   // S(l) is issued already
         for (int l = 0; l < L; ++l) {
           const bool mine = l == own && l < limit;
           const bool last = l + step >= limit;
@@ -533,24 +545,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (mine) {
-            // S_i(l) = Q_i K(l)^T, over the P that the P V before it has read
+          if (mine && !k_there) {
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t kd = kd0 + (uint64_t)(slot * (TL::kBytes >> 4));
-#pragma unroll
-              for (int x = 0; x < DH / 16; ++x)
-                umma_bf16(tm_s, qd + (uint64_t)(((x >> 2) * TL::kQHalf + (x & 3) * 32) >> 4),
-                          kd + (uint64_t)(((x >> 2) * 1024 + (x & 3) * 32) >> 4), idesc_s, x > 0);
+              issue_s(slot);
               umma_commit(&sh.s_full[i]);
               umma_commit(&sh.empty[slot]);
-              if (last) {
-                umma_commit(&sh.q_empty[qi]);
-                if (pair) umma_commit(&sh.q_empty[qi]);   // one for each issuer
-              }
+              if (last) release_q();
               if (l == 0 && n == 0) DLM_TRACE_MARK(3);
             }
-          } else if (lane == 0) {
+          } else if (!mine && lane == 0) {
             mbar_arrive(&sh.empty[slot]);
           }
           // the V check may look at V(l): both issuers are done with what its slot held
@@ -571,12 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = ok && wait(&sh.o_empty[i], no, abort_flag);
               no ^= 1;
             }
-            // two row tiles: the next K first, so that its S follows at once
+            // two row tiles: the next K first, so that its S follows P V at once
             k_there = pair && !last;
-            if (k_there) {
-              const bool wrap = slot + 1 == NS;
-              ok = ok && wait(&sh.full[wrap ? 0 : slot + 1], phase ^ (wrap ? 1u : 0u), abort_flag);
-            }
+            const uint32_t ks = slot + 1 == NS ? 0 : slot + 1;
+            if (k_there) ok = ok && wait(&sh.full[ks], phase ^ (ks == 0 ? 1u : 0u), abort_flag);
             // in two halves: the first runs during the second's exponentials
             const uint64_t vd = vd0 + (uint64_t)(slot * (TL::kBytes >> 4));
 #pragma unroll 1
@@ -591,6 +593,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    vd + (uint64_t)((h * 8 + x * 2) * TL::kGroup >> 4), idesc_o,
                                    l != first || h > 0 || x > 0);
                 if (h == 1) {
+                  if (k_there) {
+                    issue_s(ks);
+                    umma_commit(&sh.s_full[i]);
+                    umma_commit(&sh.empty[ks]);
+                    if (l + 1 + step >= limit) release_q();
+                  }
                   umma_commit(&sh.empty[slot]);
                   if (last) umma_commit(&sh.o_full[i]);
                 }
@@ -987,11 +995,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16_u(s_col + y * 16, w);
           };
           uint32_t ra[32], rb[32];
+          tmem_ld32_nowait(s_col, ra);
           if (!take_turn(x)) {
             ok = false;
             break;
           }
-          tmem_ld32_nowait(s_col, ra);
 #pragma unroll 1
           for (int y = 0; y < kKeys / 32; y += 2) {
             tmem_wait_ld();
