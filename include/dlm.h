@@ -498,7 +498,7 @@ int dlm_check(dlm_ctx *ctx, void *stream);
  * last launch of each kind; 0 = not reached.  Kinds: 0 embed, 1 QKV GEMM,
  * 2 QKV epilogue, 3 attention, 4 attention combine, 5 Wo GEMM, 6 Wo
  * epilogue, 7 row quantisation, 8 LM head, 9 commit, 10
- * paged attention, 11 its join.  The default build
+ * paged attention.  The default build
  * exports the same calls; they return DLM_ESTATE. */
 
 /* Table dimensions: kinds x ctas (linear CTA index) x slots. */

@@ -52,8 +52,7 @@ enum TraceKind {
   TRACE_LM_HEAD = 8,
   TRACE_COMMIT = 9,
   TRACE_PAGED = 10,
-  TRACE_PAGED_JOIN = 11,
-  TRACE_KINDS_USED = 12
+  TRACE_KINDS_USED = 11
 };
 #ifdef DLM_TRACE
 // each translation unit's table (see DLM_TRACE_STORAGE)
@@ -273,11 +272,12 @@ struct PagedAttn {
   void* work;
   int* err;
 };
-cudaError_t paged_attention_simt(const PagedAttn& a, cudaStream_t st);   // any type
 
-// ---- paged_attention.cu: bf16 on the tensor cores ---------------------------------
+// ---- paged_attention.cu: bf16 on the tensor cores; paged_attention_f32.cu ------------
 size_t paged_attention_work(int Dh, int num_sms);   // bytes of workspace
 cudaError_t paged_attention_tc(const PagedAttn& a, int num_sms, cudaStream_t st);
+size_t paged_attention_f32_work(int Dh, int num_sms);
+cudaError_t paged_attention_f32(const PagedAttn& a, int num_sms, cudaStream_t st);
 
 // ---- dlm_api.cu: errors and driver entry points for context-free calls -----------
 int api_fail(int code, const char* what);

@@ -4,7 +4,6 @@
 #include <climits>
 
 #include <cooperative_groups.h>
-#include <math_constants.h>
 
 #include "kernels.h"
 
@@ -215,81 +214,6 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const PagedKV c, const ui
   reinterpret_cast<uint4*>(c.v)[dst] = *reinterpret_cast<const uint4*>(v + t * v_stride + j * 16);
 }
 
-// ---------------------------------------------------------------------------
-// Attention, one warp per (query row, head): online softmax over the visible
-// keys, Dh / 32 dimensions a lane.
-// ---------------------------------------------------------------------------
-// offsets ascending within the rows, a length that the table can hold
-__device__ __forceinline__ bool sequence_ok(const PagedAttn& a, int b) {
-  const int c0 = a.cu[b], c1 = a.cu[b + 1], ctx = a.ctx[b];
-  return c0 >= 0 && c0 <= c1 && c1 <= a.T && ctx >= 0 &&
-         (long long)ctx <= ((long long)a.W << a.c.page_shift);
-}
-
-template <typename T, int DH>
-__global__ void __launch_bounds__(128) attend_kernel(const PagedAttn a) {
-  constexpr int E = DH / 32;
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x)
-      if (!sequence_ok(a, b)) raise_error(a.err, DLM_EBOUNDS);
-  const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (wid >= (int64_t)a.T * a.H) return;
-  const int t = (int)(wid / a.H), h = (int)(wid % a.H);
-  // the sequence of this row
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid] <= t)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int b = lo;
-  const int n = a.cu[b + 1] - a.cu[b], i = t - a.cu[b], ctx = a.ctx[b];
-  const int P = 1 << a.c.page_shift;
-  if (i < 0 || i >= n || !sequence_ok(a, b)) return;
-  const int pos = ctx - n + i;
-  int limit = ctx;
-  if (a.block > 0) limit = pos < 0 ? 0 : (int)min((long long)ctx, ((long long)pos / a.block + 1) * a.block);
-  const int g = h / (a.H / a.c.Hkv);
-  const T* q = reinterpret_cast<const T*>(a.q) + t * a.q_stride + h * DH;
-  float qr[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qr[e] = to_f32(q[e * 32 + lane]) * a.scale;
-    acc[e] = 0.f;
-  }
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int j = 0; j < limit; ++j) {
-    const int page = a.table[(size_t)b * a.W + (j >> a.c.page_shift)];
-    if (page < 0 || page >= a.c.n_pages) {
-      if (lane == 0) raise_error(a.err, DLM_EBOUNDS);
-      continue;
-    }
-    const size_t row = (((size_t)page * a.c.Hkv + g) << a.c.page_shift) + (j & (P - 1));
-    const T* kp = reinterpret_cast<const T*>(a.c.k) + row * DH;
-    const T* vp = reinterpret_cast<const T*>(a.c.v) + row * DH;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qr[e], to_f32(kp[e * 32 + lane]), s);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float m_new = fmaxf(m, s);
-    const float base = m_new == -CUDART_INF_F ? 0.f : m_new;
-    const float alpha = expf(m - base), p = expf(s - base);
-    l = l * alpha + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * alpha + p * to_f32(vp[e * 32 + lane]);
-    m = m_new;
-  }
-  T* o = reinterpret_cast<T*>(a.o) + t * a.o_stride + h * DH;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e * 32 + lane] = from_f32<T>(acc[e] * inv);
-  if (a.lse != nullptr && lane == 0) a.lse[(size_t)t * a.H + h] = l == 0.f ? -CUDART_INF_F : m + logf(l);
-}
-
 }  // namespace
 
 cudaError_t paged_resize(const PagedResize& a, cudaStream_t st) {
@@ -326,23 +250,6 @@ cudaError_t paged_kv_write(const PagedKV& c, const void* k, const void* v, int64
   kv_write_kernel<<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(
       c, (const uint8_t*)k, (const uint8_t*)v, k_stride * c.esize, v_stride * c.esize, slots, n,
       err);
-  return cudaGetLastError();
-}
-
-cudaError_t paged_attention_simt(const PagedAttn& a, cudaStream_t st) {
-  const int64_t warps = (int64_t)a.T * a.H;
-  const unsigned grid = (unsigned)((warps + 3) / 4);
-  const bool bf = a.c.esize == 2;
-  if (bf && a.c.Dh == 64)
-    attend_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(a);
-  else if (bf)
-    attend_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(a);
-  else if (a.c.Dh == 32)
-    attend_kernel<float, 32><<<grid, 128, 0, st>>>(a);
-  else if (a.c.Dh == 64)
-    attend_kernel<float, 64><<<grid, 128, 0, st>>>(a);
-  else
-    attend_kernel<float, 128><<<grid, 128, 0, st>>>(a);
   return cudaGetLastError();
 }
 

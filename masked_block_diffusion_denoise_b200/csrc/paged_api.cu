@@ -83,6 +83,11 @@ const char* heads_problem(const dlm_paged_cache* c, int n_heads) {
   return nullptr;
 }
 
+size_t work_of(const dlm_paged_cache* c, const PagedDevice* d) {
+  return c->dtype == DLM_BF16 ? paged_attention_work(c->head_dim, d->num_sms)
+                              : paged_attention_f32_work(c->head_dim, d->num_sms);
+}
+
 PagedKV kv_of(const dlm_paged_cache* c) {
   return PagedKV{c->k, c->v, c->n_pages, page_shift(c->page_size), c->n_kv_heads, c->head_dim,
                  c->dtype == DLM_BF16 ? 2 : 4};
@@ -162,12 +167,9 @@ int dlm_paged_attention_workspace(const dlm_paged_cache* cache, int n_heads, siz
   if (bytes == nullptr) return api_fail(DLM_EINVAL, "paged_attention_workspace: NULL pointer argument");
   if (const char* why = cache_problem(cache)) return api_fail(DLM_EINVAL, why);
   if (const char* why = heads_problem(cache, n_heads)) return api_fail(DLM_EINVAL, why);
-  *bytes = 256;
-  if (cache->dtype == DLM_BF16) {
-    PagedDevice* d = nullptr;
-    if (int rc = paged_device(&d)) return rc;
-    *bytes = paged_attention_work(cache->head_dim, d->num_sms);
-  }
+  PagedDevice* d = nullptr;
+  if (int rc = paged_device(&d)) return rc;
+  *bytes = work_of(cache, d);
   return DLM_OK;
 }
 
@@ -197,12 +199,12 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
     return api_fail(DLM_EINVAL, why);
   if ((long long)n_tokens * n_heads > INT_MAX)
     return api_fail(DLM_EINVAL, "paged_attention: n_tokens * n_heads exceeds 2^31 - 1");
-  if (workspace_bytes < 256)   // the least that any cache needs
+  if (workspace_bytes < 4096)   // less than any cache needs
     return api_fail(DLM_EINVAL, "paged_attention: the workspace is too small");
   PagedDevice* d = nullptr;
   int dev = 0;
   if (int rc = paged_device(&d, &dev)) return rc;
-  if (c.esize == 2 && workspace_bytes < paged_attention_work(c.Dh, d->num_sms))
+  if (workspace_bytes < work_of(cache, d))
     return api_fail(DLM_EINVAL, "paged_attention: the workspace is too small");
   for (const void* p : {q, (const void*)o, (const void*)lse, (const void*)cu_q,
                         (const void*)ctx_lens, (const void*)block_table, (const void*)workspace,
@@ -213,7 +215,8 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
               n_tokens, n_heads, mask_block,
               scale > 0.f ? scale : (float)(1.0 / sqrt((double)c.Dh)), workspace, d->err};
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = c.esize == 2 ? paged_attention_tc(a, d->num_sms, st) : paged_attention_simt(a, st);
+  cudaError_t e = c.esize == 2 ? paged_attention_tc(a, d->num_sms, st)
+                                : paged_attention_f32(a, d->num_sms, st);
   if (e != cudaSuccess)
     return api_cuda_fail("paged_attention launch", e);
   return DLM_OK;

@@ -18,11 +18,7 @@
 // halves, rows / 8 groups, 1 page): whatever the page size (>= 8), a 128-key
 // tile in shared memory is [16 groups of 8 rows][half][8 rows][128 bytes], with
 // one stride between 8-row groups, which is what the MMA descriptors need.
-#include <math_constants.h>
-
-#include <type_traits>
-
-#include "kernels.h"
+#include "paged_attn.cuh"
 
 namespace dlm {
 
@@ -58,30 +54,6 @@ struct Tile {
   static constexpr int kSlots = DH == 128 ? 5 : 10;      // ring of K and V tiles
 };
 
-struct Item {
-  int b, g;
-  int row0, npos;      // first row of q, positions of the item
-  int pos0, ctx;       // position of the first row, keys of the sequence
-  int ts, te;          // key tiles of this CTA
-  int kt0, pair;       // key tiles of row tile 0; two row tiles
-  int whole;           // every key tile is here: write the result
-  int slot;            // partial slot (1: the item starts here)
-  int fix;             // keys that every row sees; V behind them is checked
-  int poison;          // ... and holds an infinity or NaN
-  int valid;           // 0: no more items
-  int pad;
-};
-static_assert(sizeof(Item) == 64, "");
-
-// what the join needs to know of a CTA's cut items
-struct Meta {
-  int tail;            // an item starts here and is cut
-  int row0, npos, g, pair;
-  int head;            // a partial of an item that started earlier
-  int head_ends;       // ... whose last key tile is here
-  int pad;
-};
-
 template <int DH>
 struct Smem {
   static constexpr int kQ = 0;
@@ -101,22 +73,6 @@ struct Smem {
   static constexpr int kBytes = kTail + (int)sizeof(Rest);
 };
 static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory");
-
-struct Params {
-  const int32_t* cu;
-  const int32_t* ctx;
-  const int32_t* table;
-  const __nv_bfloat16* v;
-  __nv_bfloat16* o;
-  int64_t o_stride;
-  float* lse;
-  float* part;         // [cta][2][2 * kRows][DH]
-  float2* ml;          // [cta][2][2 * kRows]
-  Meta* meta;          // [cta]
-  int* err;
-  int W, B, T, H, Hkv, G, npos, block, n_pages, page_shift;
-  float scale_log2;
-};
 
 // matrix descriptors of a 128-row tile whose 8-row groups are `group` bytes
 // apart (128-byte swizzle): K-major (rows = N), and MN-major (rows = K, 64-element
@@ -160,48 +116,6 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
-__device__ __noinline__ int block_end(int p, int ctx, int block) {
-  return (int)min((long long)ctx, ((long long)(p / block) + 1) * block);
-}
-// keys [0, n) that the row at position p sees
-__device__ __forceinline__ int visible(int p, int ctx, int block) {
-  if (block == 0) return ctx;
-  if (p < 0) return 0;
-  if (block == 1) return min(ctx, p + 1);
-  return block_end(p, ctx, block);
-}
-
-// The cost of a sequence's items, in keys: item j (2 * npos positions) costs the
-// keys below its last row's position (its block's end is not counted) plus
-// kItemCost.  cum(j) is the cost of the items before j.
-struct SeqCost {
-  long long base;   // position of row 0
-  int n, ctx, pp, items, j0;
-  bool masked;
-  __device__ SeqCost(int n_, int ctx_, int pp_, int block)
-      : base((long long)ctx_ - n_), n(n_), ctx(ctx_), pp(pp_), masked(block != 0) {
-    items = (int)(((uint32_t)n + (uint32_t)pp - 1u) / (uint32_t)pp);
-    // items wholly before position 0 (masked, base < 0): no keys
-    j0 = base < 0 ? min(max(items - 1, 0), (int)(-base / pp)) : 0;
-  }
-  __device__ long long cum(int j) const {
-    if (!masked) return (long long)j * (ctx + kItemCost);
-    const bool end = j == items && j > 0;
-    if (end) --j;
-    long long c = (long long)kItemCost * j;
-    if (j > j0)
-      c += (j - j0) * base +
-           (long long)pp * (((long long)j * (j + 1) - (long long)j0 * (j0 + 1)) / 2);
-    if (end) c += ctx + kItemCost;
-    return c;
-  }
-};
-
-__device__ __forceinline__ bool seq_ok(const Params& p, int c0, int c1, int ctx) {
-  return c0 >= 0 && c0 <= c1 && c1 <= p.T && ctx >= 0 &&
-         (long long)ctx <= ((long long)p.W << p.page_shift);
-}
-
 __device__ __forceinline__ float fmax3f(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -239,7 +153,7 @@ __device__ __noinline__ void add_poison(const Params& p, const Item& it, int k0,
     const int page = p.table[(size_t)it.b * p.W + (k >> p.page_shift)];
     if (page < 0 || page >= p.n_pages) continue;
     const __nv_bfloat16* row =
-        p.v + ((((size_t)page * p.Hkv + it.g) << p.page_shift) + (k & mask)) * DH + c0;
+        (const __nv_bfloat16*)p.v + ((((size_t)page * p.Hkv + it.g) << p.page_shift) + (k & mask)) * DH + c0;
 #pragma unroll 1
     for (int j = 0; j < 16; ++j) {
       const float x = __bfloat162float(row[j]);
@@ -303,87 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the join may be set up while this grid runs (it waits for the grid's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's range of the work ----
-  // scan of the sequences' costs (consecutive sequences per thread), then the
-  // owners of the range's two ends turn them into (KV head, sequence, item, tile)
-  {
-    long long* scan = reinterpret_cast<long long*>(ring);   // a sum per warp; free until the first load
-    const int pp = 2 * p.npos;
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-      const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), ctx = __ldg(p.ctx + b);
-      if (!seq_ok(p, c0, c1, ctx)) {
-        if (blockIdx.x == 0) raise_error(p.err, DLM_EBOUNDS);
-        continue;
-      }
-      const SeqCost s(c1 - c0, ctx, pp, p.block);
-      mine += s.cum(s.items);
-    }
-    long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 31) scan[warp] = incl;
-    if (tid < 4) sh.start[tid] = sh.stop[tid] = 0;
-    __syncthreads();
-    long long before = 0, w1 = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w == warp) before = w1;
-      w1 += scan[w];
-    }
-    const long long first = before + incl - mine;   // cost before sequence b0
-    const long long total = w1 * p.Hkv;
-    // (doubles: every CTA computes the same edges, and no 64-bit divisions)
-    const int ctas = (int)max(1.0, min((double)gridDim.x, floor((double)total * (1.0 / kMinKeys))));
-    const double share = (double)total / ctas;
-    auto edge = [&](int k) { return k >= ctas ? total : min(total, (long long)(share * k)); };
-    const long long u[2] = {edge(blockIdx.x), edge(blockIdx.x + 1)};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      int* dst = e == 0 ? sh.start : sh.stop;
-      if (w1 == 0 || u[e] >= total) {
-        if (tid == 0) dst[0] = p.Hkv;   // the end
-        continue;
-      }
-      int g = (int)((double)u[e] / (double)w1);   // the quotient, or one off it
-      g -= g * w1 > u[e];
-      g += (g + 1) * w1 <= u[e];
-      long long r = u[e] - g * w1 - first;
-      if (r < 0 || r >= mine) continue;
-      for (int b = b0; b < b1; ++b) {
-        const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), ctx = __ldg(p.ctx + b);
-        if (!seq_ok(p, c0, c1, ctx)) continue;
-        const SeqCost s(c1 - c0, ctx, pp, p.block);
-        const long long c = s.cum(s.items);
-        if (r >= c) {
-          r -= c;
-          continue;
-        }
-        int lo = 0, hi = s.items;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (s.cum(mid) <= r)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        const long long at = r - s.cum(lo), cost = s.cum(lo + 1) - s.cum(lo);
-        const int i1 = (int)min((long long)s.n, (long long)(lo + 1) * pp);
-        const int kt = (visible(ctx - s.n + i1 - 1, ctx, p.block) + kKeys - 1) / kKeys;
-        dst[0] = g;
-        dst[1] = b;
-        dst[2] = lo;
-        // < kt; 0: the item starts in this range
-        dst[3] = max(0, min(kt - 1, (int)((double)at * kt / (double)cost)));
-        break;
-      }
-    }
-  }
+  // ---- this CTA's range of the work (the scan's scratch is the ring, free until
+  // the first load) ----
+  find_range<kThreads>(p, kKeys, kItemCost, kMinKeys, reinterpret_cast<long long*>(ring), sh.start,
+                       sh.stop);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -622,93 +459,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(&sh.fin[i], 0, nullptr);
     } else if (warp == kScheduler) {
       // ---------------- scheduler: the range's items, one descriptor each ----------------
-      const int g1 = sh.stop[0], b_end = sh.stop[1], j_end = sh.stop[2], t_end = sh.stop[3];
-      int g = sh.start[0], b = sh.start[1], j = sh.start[2], t0 = sh.start[3];
-      Meta meta = {};
-      int cb = -1;   // 32 sequences in registers, one per lane
-      int l0 = 0, l1 = 0, lc = 0;
+      Walker walk(sh.start, sh.stop);
       uint32_t n = 0;
-      bool ok = true;
       for (;;) {
-        bool more = g < g1 || (g == g1 && g < p.Hkv && (b < b_end || (b == b_end && (j < j_end ||
-                                                        (j == j_end && t_end > 0)))));
-        Item it = {};
-        if (more) {
-          if (b >> 5 != cb) {
-            cb = b >> 5;
-            const int bb = cb * 32 + lane;
-            const bool in = bb < p.B;
-            l0 = in ? __ldg(p.cu + bb) : 0;
-            l1 = in ? __ldg(p.cu + bb + 1) : 0;
-            lc = in ? __ldg(p.ctx + bb) : 0;
-            if (!in || !seq_ok(p, l0, l1, lc)) l1 = l0 = 0;
-          }
-          const int c0 = __shfl_sync(0xffffffffu, l0, b & 31);
-          const int c1 = __shfl_sync(0xffffffffu, l1, b & 31);
-          const int ctx = __shfl_sync(0xffffffffu, lc, b & 31);
-          const int len = c1 - c0, pp = 2 * p.npos;
-          if ((long long)j * pp >= len) {   // the next sequence, then the next KV head
-            j = 0;
-            t0 = 0;
-            // over empty sequences of this chunk at once
-            const uint32_t full = __ballot_sync(0xffffffffu, l1 > l0);
-            const uint32_t later = (b & 31) == 31 ? 0u : full & (0xffffffffu << ((b & 31) + 1));
-            b = later != 0 ? (b & ~31) + __ffs(later) - 1 : (b & ~31) + 32;
-            if (b >= p.B) {
-              b = 0;
-              ++g;
-            }
-            continue;
-          }
-          const int i0 = j * pp;
-          it.b = b;
-          it.g = g;
-          it.row0 = c0 + i0;
-          it.npos = min(pp, len - i0);
-          it.pos0 = ctx - len + i0;
-          it.ctx = ctx;
-          it.pair = it.npos > p.npos;
-          const int last0 = it.pos0 + min(it.npos, p.npos) - 1;
-          it.kt0 = (visible(last0, ctx, p.block) + kKeys - 1) / kKeys;
-          const int kt = (visible(it.pos0 + it.npos - 1, ctx, p.block) + kKeys - 1) / kKeys;
-          const bool stops = g == g1 && b == b_end && j == j_end;
-          it.ts = t0;
-          it.te = stops ? t_end : kt;
-          it.whole = it.ts == 0 && it.te == kt;
-          it.slot = it.ts == 0;
-          it.fix = visible(it.pos0, ctx, p.block);
-          it.valid = 1;
-          const bool empty_cut = !it.whole && it.ts >= it.te;   // nothing of a cut item
-          if (!it.whole) {
-            if (it.ts == 0) {
-              meta.tail = 1;
-              meta.row0 = it.row0;
-              meta.npos = it.npos;
-              meta.g = g;
-              meta.pair = it.pair;
-            } else {
-              meta.head = !empty_cut;
-              meta.head_ends = it.te == kt;
-            }
-          }
-          t0 = 0;
-          ++j;
-          if (empty_cut) continue;
-        }
+        const Item it = walk.next(p, kKeys, lane);
         const int ds = n % kDescs;
-        if (!mbar_wait_bounded(&sh.d_empty[ds], ((n / kDescs) & 1) ^ 1, abort_flag)) {
-          ok = false;
-          break;
-        }
+        if (!mbar_wait_bounded(&sh.d_empty[ds], ((n / kDescs) & 1) ^ 1, abort_flag)) break;
         if (lane == 0) {
           sh.item[ds] = it;
           mbar_arrive(&sh.d_full[ds]);
         }
         ++n;
-        if (!more) break;
+        if (!it.valid) break;
       }
-      (void)ok;
-      if (lane == 0) p.meta[blockIdx.x] = meta;
+      if (lane == 0) p.meta[blockIdx.x] = walk.meta;
     } else {
       // ---------------- writers: V check, results ----------------
       // A hidden key has probability 0, but 0 x infinity is NaN: in tiles with hidden
@@ -813,11 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             w1 *= inv;
           }
           const size_t prow =
-              ((size_t)blockIdx.x * 2 + it.slot) * (2 * kRows) + (pair ? i * kRows : 0) + row;
+              ((size_t)blockIdx.x * 2 + it.slot) * kSlotRows + (pair ? i * kRows : 0) + row;
           const int64_t grow = (int64_t)it.row0 + pos;
           const int head = it.g * p.G + rh;
           if (__any_sync(0xffffffffu, live)) {
-            uint4* dst_o = reinterpret_cast<uint4*>(p.o + grow * p.o_stride + (int64_t)head * DH);
+            uint4* dst_o = reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + grow * p.o_stride + (int64_t)head * DH);
             float4* dst_p = reinterpret_cast<float4*>(p.part + prow * DH);
             // 16 columns at a time: little code, which runs once per item
 #pragma unroll 1
@@ -1054,113 +818,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *abort_flag) raise_error(p.err, DLM_ETIMEOUT);
 }
 
-// Joins the partials of an item that starts in CTA c: c's own, then those of
-// c + 1, ... up to the CTA where it ends, in that order.  A warp joins
-// kJoinWarpRows rows at once, lane = DH / 32 columns: the partials' maxima and
-// sums 32 at a time in the lanes, then their rows in batches of independent
-// loads (the join is a chain of loads, so it is the number of links that counts).
-constexpr int kJoinWarpRows = 4, kJoinRows = 8 * kJoinWarpRows;
-template <int DH>
-__global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_ctas) {
-  constexpr int E = DH / 32, R = kJoinWarpRows;
-  using Vec = typename std::conditional<E == 4, float4, float2>::type;
-  DLM_TRACE_CTA(TRACE_PAGED_JOIN);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Meta me = p.meta[c];
-  // rows r0 + 8 u of row tile `tile`; those in use are the tile's first ones
-  const int tile = blockIdx.y * kJoinRows / kRows;
-  const int r0 = blockIdx.y * kJoinRows + warp;
-  const int used = tile * kRows + min(p.npos, me.npos - tile * p.npos) * p.G;
-  if (!me.tail || r0 >= used) return;
-  float m[R], l[R], acc[R][E];
-#pragma unroll
-  for (int u = 0; u < R; ++u) {
-    m[u] = -CUDART_INF_F;
-    l[u] = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[u][e] = 0.f;
-  }
-  bool ends = false;
-  for (int k0 = c; k0 < n_ctas && !ends; k0 += 32) {
-    const int k = k0 + lane;
-    const bool next = k < n_ctas && k > c;
-    const bool here = k == c || (next && p.meta[k].head != 0);
-    const uint32_t stops = __ballot_sync(0xffffffffu, next && p.meta[k].head_ends != 0);
-    ends = stops != 0;
-    const int n = ends ? __ffs(stops) : min(32, n_ctas - k0);   // partials of this batch
-    float w[R];
-    {
-      float2 v[R];
-#pragma unroll
-      for (int u = 0; u < R; ++u)
-        v[u] = here && lane < n && r0 + 8 * u < used ? p.ml[((size_t)k * 2 + (k == c)) * (2 * kRows) + r0 + 8 * u]
-                                : make_float2(-CUDART_INF_F, 0.f);
-#pragma unroll
-      for (int u = 0; u < R; ++u) {
-        float bm = v[u].x;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
-        const float m_new = fmaxf(m[u], bm);
-        const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // no key seen so far
-        const float old = fast_exp2(m[u] - base);
-        w[u] = fast_exp2(v[u].x - base);
-        float bl = w[u] == 0.f ? 0.f : w[u] * v[u].y;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) bl += __shfl_xor_sync(0xffffffffu, bl, d);
-        l[u] = l[u] * old + bl;
-        m[u] = m_new;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[u][e] *= old;
-      }
-    }
-    constexpr int kB = 4;
-    for (int s = 0; s < n; s += kB) {
-      Vec y[R][kB];
-      float ws[R][kB];
-#pragma unroll
-      for (int x = 0; x < kB; ++x) {
-        const size_t row =
-            ((size_t)(k0 + s + x) * 2 + (k0 + s + x == c)) * (2 * kRows) + r0;
-#pragma unroll
-        for (int u = 0; u < R; ++u) {
-          ws[u][x] = __shfl_sync(0xffffffffu, w[u], (s + x) & 31);
-          if (s + x >= n) ws[u][x] = 0.f;
-          // (a weight of 0: no partial, or rows behind the item's last)
-          if (ws[u][x] != 0.f)
-            y[u][x] = *reinterpret_cast<const Vec*>(p.part + (row + 8 * u) * DH + lane * E);
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < kB; ++x)
-#pragma unroll
-        for (int u = 0; u < R; ++u)
-          if (ws[u][x] != 0.f) {
-            const float* f = reinterpret_cast<const float*>(&y[u][x]);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[u][e] = fmaf(ws[u][x], f[e], acc[u][e]);
-          }
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < R; ++u) {
-    if (r0 + 8 * u >= used) continue;
-    const int x = r0 + 8 * u - tile * kRows;
-    const int rp = x / p.G, rh = x - rp * p.G, pos = tile * p.npos + rp;
-    const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
-    const int64_t grow = (int64_t)me.row0 + pos;
-    const int head = me.g * p.G + rh;
-    __nv_bfloat16* dst = p.o + grow * p.o_stride + (int64_t)head * DH + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<__nv_bfloat162*>(dst + e) =
-          __floats2bfloat162_rn(acc[u][e] * inv, acc[u][e + 1] * inv);
-    if (p.lse != nullptr && lane == 0)
-      p.lse[(size_t)grow * p.H + head] =
-          l[u] == 0.f ? -CUDART_INF_F : (m[u] + log2f(l[u])) * 0.69314718055994531f;
-  }
-}
-
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -1176,9 +833,6 @@ bool encode(CUtensorMap* m, void* base, int rank, const cuuint64_t* dims, const 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t part_bytes(int ctas, int Dh) { return (size_t)ctas * 2 * 2 * kRows * Dh * sizeof(float); }
-size_t ml_bytes(int ctas) { return (size_t)ctas * 2 * 2 * kRows * sizeof(float2); }
-
 template <int DH>
 cudaError_t launch(const PagedAttn& a, int num_sms, cudaStream_t st) {
   static DeviceOnce once;
@@ -1187,31 +841,9 @@ cudaError_t launch(const PagedAttn& a, int num_sms, cudaStream_t st) {
                                 Smem<DH>::kBytes);
   });
   if (e != cudaSuccess) return e;
-  Params p;
-  p.cu = a.cu;
-  p.ctx = a.ctx;
-  p.table = a.table;
-  p.v = (const __nv_bfloat16*)a.c.v;
-  p.o = (__nv_bfloat16*)a.o;
-  p.o_stride = a.o_stride;
-  p.lse = a.lse;
-  uint8_t* work = (uint8_t*)a.work;
-  p.part = (float*)work;
-  p.ml = (float2*)(work + part_bytes(num_sms, DH));
-  p.meta = (Meta*)(work + part_bytes(num_sms, DH) + ml_bytes(num_sms));
-  p.err = a.err;
-  p.W = a.W;
-  p.B = a.B;
-  p.T = a.T;
-  p.H = a.H;
-  p.Hkv = a.c.Hkv;
-  p.G = a.H / a.c.Hkv;
+  Params p = make_params(a, num_sms);
   p.npos = kRows / p.G;
-  p.block = a.block;
-  p.n_pages = a.c.n_pages;
-  p.page_shift = a.c.page_shift;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
-
+  p.positions = 2 * p.npos;
   const cuuint64_t rows = (cuuint64_t)1 << a.c.page_shift;
   const cuuint64_t kd[5] = {64, 8, DH / 64, rows / 8, (cuuint64_t)a.c.n_pages * a.c.Hkv};
   const cuuint64_t ks[4] = {DH * 2, 128, DH * 16, rows * DH * 2};
@@ -1225,13 +857,13 @@ cudaError_t launch(const PagedAttn& a, int num_sms, cudaStream_t st) {
     return cudaErrorInvalidValue;
   paged_attn_kernel<DH><<<num_sms, kThreads, Smem<DH>::kBytes, st>>>(tmK, tmV, tmQ, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_pdl(paged_join_kernel<DH>, dim3(num_sms, 2 * kRows / kJoinRows), dim3(256), 0, st, p, num_sms);
+  return launch_join<__nv_bfloat16, DH>(p, num_sms, kSlotRows, st);
 }
 
 }  // namespace
 
 size_t paged_attention_work(int Dh, int num_sms) {
-  return part_bytes(num_sms, Dh) + ml_bytes(num_sms) + (size_t)num_sms * sizeof(Meta);
+  return work_bytes(num_sms, Dh);
 }
 
 cudaError_t paged_attention_tc(const PagedAttn& a, int num_sms, cudaStream_t st) {

@@ -1,0 +1,432 @@
+// Parts shared by the paged attention kernels (bf16 on the tensor cores, float32
+// on the CUDA cores): what a row sees, how the work is cut into one range per
+// CTA, the walk over a range's items, and the join of items that were cut.
+#pragma once
+
+#include <math_constants.h>
+
+#include <type_traits>
+
+#include "kernels.h"
+
+namespace dlm {
+
+namespace {
+
+constexpr int kSlotRows = 256;   // rows of a partial in the workspace
+
+// A piece of work: up to `positions` consecutive positions of a sequence for one
+// KV head (with that head's G query heads), and a range of their key tiles.
+struct Item {
+  int b, g;
+  int row0, npos;      // first row of q, positions of the item
+  int pos0, ctx;       // position of the first row, keys of the sequence
+  int ts, te;          // key tiles of this CTA
+  int kt0, pair;       // key tiles of row tile 0; two row tiles
+  int whole;           // every key tile is here: write the result
+  int slot;            // partial slot (1: the item starts here)
+  int fix;             // keys that every row sees; V behind them is checked
+  int poison;          // ... and holds an infinity or NaN
+  int valid;           // 0: no more items
+  int pad;
+};
+static_assert(sizeof(Item) == 64, "");
+
+// What the join needs to know of a CTA's cut items
+struct Meta {
+  int tail;            // an item starts here and is cut
+  int row0, npos, g, pair;
+  int head;            // a partial of an item that started earlier
+  int head_ends;       // ... whose last key tile is here
+  int pad;
+};
+
+struct Params {
+  const int32_t* cu;
+  const int32_t* ctx;
+  const int32_t* table;
+  const void* k;
+  const void* v;
+  const void* q;
+  int64_t q_stride;
+  void* o;
+  int64_t o_stride;
+  float* lse;
+  float* part;         // [cta][2][kSlotRows][Dh]
+  float2* ml;          // [cta][2][kSlotRows]
+  Meta* meta;          // [cta]
+  int* err;
+  int W, B, T, H, Hkv, G, npos, block, n_pages, page_shift;
+  int positions;       // of an item: npos, or 2 * npos (two row tiles)
+  float scale_log2;
+};
+
+__device__ __noinline__ int block_end(int p, int ctx, int block) {
+  return (int)min((long long)ctx, ((long long)(p / block) + 1) * block);
+}
+// keys [0, n) that the row at position p sees
+__device__ __forceinline__ int visible(int p, int ctx, int block) {
+  if (block == 0) return ctx;
+  if (p < 0) return 0;
+  if (block == 1) return min(ctx, p + 1);
+  return block_end(p, ctx, block);
+}
+
+// The cost of a sequence's items, in keys: item j (pp positions) costs the keys
+// below its last row's position (its block's end is not counted) plus item_cost
+// (loading Q, the first scores, the results).  cum(j) is the cost of the items before j.
+struct SeqCost {
+  long long base;   // position of row 0
+  int n, ctx, pp, items, j0;
+  long long item_cost;
+  bool masked;
+  __device__ SeqCost(int n_, int ctx_, int pp_, int block, int cost)
+      : base((long long)ctx_ - n_), n(n_), ctx(ctx_), pp(pp_), item_cost(cost), masked(block != 0) {
+    items = (int)(((uint32_t)n + (uint32_t)pp - 1u) / (uint32_t)pp);
+    // items wholly before position 0 (masked, base < 0): no keys
+    j0 = base < 0 ? min(max(items - 1, 0), (int)(-base / pp)) : 0;
+  }
+  __device__ long long cum(int j) const {
+    if (!masked) return (long long)j * (ctx + item_cost);
+    const bool end = j == items && j > 0;
+    if (end) --j;
+    long long c = item_cost * j;
+    if (j > j0)
+      c += (j - j0) * base +
+           (long long)pp * (((long long)j * (j + 1) - (long long)j0 * (j0 + 1)) / 2);
+    if (end) c += ctx + item_cost;
+    return c;
+  }
+};
+
+__device__ __forceinline__ bool seq_ok(const Params& p, int c0, int c1, int ctx) {
+  return c0 >= 0 && c0 <= c1 && c1 <= p.T && ctx >= 0 &&
+         (long long)ctx <= ((long long)p.W << p.page_shift);
+}
+
+// This CTA's range of the work, as (KV head, sequence, item, key tile): all items,
+// KV head by KV head, laid end to end in units of cost and cut into equal
+// shares (of at least min_keys).  A scan over the sequences' costs, consecutive
+// ones per thread; the owners of the range's two ends turn them into an item
+// and a tile.  `scan`: shared memory, a number per warp.  The caller
+// synchronises before it reads start and stop ([0] = Hkv: the end).
+template <int THREADS>
+__device__ void find_range(const Params& p, int key_tile, int item_cost, int min_keys,
+                           long long* scan, int* start, int* stop) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pp = p.positions;
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), ctx = __ldg(p.ctx + b);
+    if (!seq_ok(p, c0, c1, ctx)) {
+      if (blockIdx.x == 0) raise_error(p.err, DLM_EBOUNDS);
+      continue;
+    }
+    const SeqCost s(c1 - c0, ctx, pp, p.block, item_cost);
+    mine += s.cum(s.items);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) scan[warp] = incl;
+  if (tid < 4) start[tid] = stop[tid] = 0;
+  __syncthreads();
+  long long before = 0, w1 = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) before = w1;
+    w1 += scan[w];
+  }
+  const long long first = before + incl - mine;   // cost before sequence b0
+  const long long total = w1 * p.Hkv;
+  // (doubles: every CTA computes the same edges, and no 64-bit divisions)
+  const int ctas = (int)max(1.0, min((double)gridDim.x, floor((double)total * (1.0 / min_keys))));
+  const double share = (double)total / ctas;
+  auto edge = [&](int k) { return k >= ctas ? total : min(total, (long long)(share * k)); };
+  const long long u[2] = {edge(blockIdx.x), edge(blockIdx.x + 1)};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    int* dst = e == 0 ? start : stop;
+    if (w1 == 0 || u[e] >= total) {
+      if (tid == 0) dst[0] = p.Hkv;   // the end
+      continue;
+    }
+    int g = (int)((double)u[e] / (double)w1);   // the quotient, or one off it
+    g -= g * w1 > u[e];
+    g += (g + 1) * w1 <= u[e];
+    long long r = u[e] - g * w1 - first;
+    if (r < 0 || r >= mine) continue;
+    for (int b = b0; b < b1; ++b) {
+      const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), ctx = __ldg(p.ctx + b);
+      if (!seq_ok(p, c0, c1, ctx)) continue;
+      const SeqCost s(c1 - c0, ctx, pp, p.block, item_cost);
+      const long long c = s.cum(s.items);
+      if (r >= c) {
+        r -= c;
+        continue;
+      }
+      int lo = 0, hi = s.items;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.cum(mid) <= r)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const long long at = r - s.cum(lo), cost = s.cum(lo + 1) - s.cum(lo);
+      const int i1 = (int)min((long long)s.n, (long long)(lo + 1) * pp);
+      const int kt = (visible(ctx - s.n + i1 - 1, ctx, p.block) + key_tile - 1) / key_tile;
+      dst[0] = g;
+      dst[1] = b;
+      dst[2] = lo;
+      // < kt; 0: the item starts in this range
+      dst[3] = max(0, min(kt - 1, (int)((double)at * kt / (double)cost)));
+      break;
+    }
+  }
+}
+
+// The items of a range in order; every lane of a warp gets the same item.  meta
+// collects what the join needs of the items that the range cuts.
+struct Walker {
+  int g, b, j, t0, g1, b1, j1, t1;
+  int cb = -1, l0 = 0, l1 = 0, lc = 0;   // 32 sequences, one per lane
+  Meta meta = {};
+  __device__ Walker(const int* start, const int* stop)
+      : g(start[0]), b(start[1]), j(start[2]), t0(start[3]), g1(stop[0]), b1(stop[1]), j1(stop[2]),
+        t1(stop[3]) {}
+  __device__ Item next(const Params& p, int key_tile, int lane) {
+    for (;;) {
+      Item it = {};
+      if (!(g < g1 || (g == g1 && g < p.Hkv &&
+                       (b < b1 || (b == b1 && (j < j1 || (j == j1 && t1 > 0)))))))
+        return it;
+      if (b >> 5 != cb) {
+        cb = b >> 5;
+        const int bb = cb * 32 + lane;
+        const bool in = bb < p.B;
+        l0 = in ? __ldg(p.cu + bb) : 0;
+        l1 = in ? __ldg(p.cu + bb + 1) : 0;
+        lc = in ? __ldg(p.ctx + bb) : 0;
+        if (!in || !seq_ok(p, l0, l1, lc)) l1 = l0 = 0;
+      }
+      const int c0 = __shfl_sync(0xffffffffu, l0, b & 31);
+      const int c1 = __shfl_sync(0xffffffffu, l1, b & 31);
+      const int ctx = __shfl_sync(0xffffffffu, lc, b & 31);
+      const int len = c1 - c0;
+      if ((long long)j * p.positions >= len) {   // the next sequence, then the next KV head
+        j = 0;
+        t0 = 0;
+        // over the empty sequences of these 32 at once
+        const uint32_t full = __ballot_sync(0xffffffffu, l1 > l0);
+        const uint32_t later = (b & 31) == 31 ? 0u : full & (0xffffffffu << ((b & 31) + 1));
+        b = later != 0 ? (b & ~31) + __ffs(later) - 1 : (b & ~31) + 32;
+        if (b >= p.B) {
+          b = 0;
+          ++g;
+        }
+        continue;
+      }
+      const int i0 = j * p.positions;
+      it.b = b;
+      it.g = g;
+      it.row0 = c0 + i0;
+      it.npos = min(p.positions, len - i0);
+      it.pos0 = ctx - len + i0;
+      it.ctx = ctx;
+      it.pair = it.npos > p.npos;
+      const int last0 = it.pos0 + min(it.npos, p.npos) - 1;
+      it.kt0 = (visible(last0, ctx, p.block) + key_tile - 1) / key_tile;
+      const int kt = (visible(it.pos0 + it.npos - 1, ctx, p.block) + key_tile - 1) / key_tile;
+      const bool stops = g == g1 && b == b1 && j == j1;
+      it.ts = t0;
+      it.te = stops ? t1 : kt;
+      it.whole = it.ts == 0 && it.te == kt;
+      it.slot = it.ts == 0;
+      it.fix = visible(it.pos0, ctx, p.block);
+      it.valid = 1;
+      const bool nothing = !it.whole && it.ts >= it.te;   // no tile of a cut item
+      if (!it.whole) {
+        if (it.ts == 0) {
+          meta.tail = 1;
+          meta.row0 = it.row0;
+          meta.npos = it.npos;
+          meta.g = g;
+          meta.pair = it.pair;
+        } else {
+          meta.head = !nothing;
+          meta.head_ends = it.te == kt;
+        }
+      }
+      t0 = 0;
+      ++j;
+      if (!nothing) return it;
+    }
+  }
+};
+
+// Joins the partials of an item that starts in CTA c: c's own, then those of
+// c + 1, ... up to the CTA where it ends, in that order.  A warp joins
+// kJoinWarpRows rows at once, lane = DH / 32 columns: the partials' maxima and
+// sums 32 at a time in the lanes, then their rows in batches of independent
+// loads (the join is a chain of loads, so it is the number of links that counts).
+constexpr int kJoinWarpRows = 4, kJoinRows = 8 * kJoinWarpRows;
+template <typename T, int DH>
+__global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_ctas) {
+  constexpr int E = DH / 32, R = kJoinWarpRows;
+  using Vec = typename std::conditional<
+      E == 4, float4, typename std::conditional<E == 2, float2, float>::type>::type;
+  constexpr int kTileRows = kSlotRows / 2;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Meta me = p.meta[c];
+  // rows r0 + 8 u of row tile `tile`; those in use are the tile's first ones
+  const int tile = blockIdx.y * kJoinRows / kTileRows;
+  const int r0 = blockIdx.y * kJoinRows + warp;
+  const int used = tile * kTileRows + min(p.npos, me.npos - tile * p.npos) * p.G;
+  if (!me.tail || r0 >= used) return;
+  float m[R], l[R], acc[R][E];
+#pragma unroll
+  for (int u = 0; u < R; ++u) {
+    m[u] = -CUDART_INF_F;
+    l[u] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[u][e] = 0.f;
+  }
+  bool ends = false;
+  for (int k0 = c; k0 < n_ctas && !ends; k0 += 32) {
+    const int k = k0 + lane;
+    const bool next = k < n_ctas && k > c;
+    const bool here = k == c || (next && p.meta[k].head != 0);
+    const uint32_t stops = __ballot_sync(0xffffffffu, next && p.meta[k].head_ends != 0);
+    ends = stops != 0;
+    const int n = ends ? __ffs(stops) : min(32, n_ctas - k0);   // partials of this batch
+    float w[R];
+    {
+      float2 v[R];
+#pragma unroll
+      for (int u = 0; u < R; ++u)
+        v[u] = here && lane < n && r0 + 8 * u < used ? p.ml[((size_t)k * 2 + (k == c)) * kSlotRows + r0 + 8 * u]
+                                : make_float2(-CUDART_INF_F, 0.f);
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        float bm = v[u].x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
+        const float m_new = fmaxf(m[u], bm);
+        const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // no key seen so far
+        const float old = fast_exp2(m[u] - base);
+        w[u] = fast_exp2(v[u].x - base);
+        float bl = w[u] == 0.f ? 0.f : w[u] * v[u].y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) bl += __shfl_xor_sync(0xffffffffu, bl, d);
+        l[u] = l[u] * old + bl;
+        m[u] = m_new;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[u][e] *= old;
+      }
+    }
+    constexpr int kB = 4;
+    for (int s = 0; s < n; s += kB) {
+      Vec y[R][kB];
+      float ws[R][kB];
+#pragma unroll
+      for (int x = 0; x < kB; ++x) {
+        const size_t row =
+            ((size_t)(k0 + s + x) * 2 + (k0 + s + x == c)) * kSlotRows + r0;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          ws[u][x] = __shfl_sync(0xffffffffu, w[u], (s + x) & 31);
+          if (s + x >= n) ws[u][x] = 0.f;
+          // (a weight of 0: no partial, or rows behind the item's last)
+          if (ws[u][x] != 0.f)
+            y[u][x] = *reinterpret_cast<const Vec*>(p.part + (row + 8 * u) * DH + lane * E);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kB; ++x)
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+          if (ws[u][x] != 0.f) {
+            const float* f = reinterpret_cast<const float*>(&y[u][x]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[u][e] = fmaf(ws[u][x], f[e], acc[u][e]);
+          }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < R; ++u) {
+    if (r0 + 8 * u >= used) continue;
+    const int x = r0 + 8 * u - tile * kTileRows;
+    const int rp = x / p.G, rh = x - rp * p.G, pos = tile * p.npos + rp;
+    const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
+    const int64_t grow = (int64_t)me.row0 + pos;
+    const int head = me.g * p.G + rh;
+    T* dst = (T*)p.o + grow * p.o_stride + (int64_t)head * DH + lane * E;
+    if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) dst[e] = acc[u][e] * inv;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<__nv_bfloat162*>(dst + e) =
+            __floats2bfloat162_rn(acc[u][e] * inv, acc[u][e + 1] * inv);
+    }
+    if (p.lse != nullptr && lane == 0)
+      p.lse[(size_t)grow * p.H + head] =
+          l[u] == 0.f ? -CUDART_INF_F : (m[u] + log2f(l[u])) * 0.69314718055994531f;
+  }
+}
+
+inline size_t part_bytes(int ctas, int Dh) {
+  return (size_t)ctas * 2 * kSlotRows * Dh * sizeof(float);
+}
+inline size_t ml_bytes(int ctas) { return (size_t)ctas * 2 * kSlotRows * sizeof(float2); }
+inline size_t work_bytes(int ctas, int Dh) {
+  return part_bytes(ctas, Dh) + ml_bytes(ctas) + (size_t)ctas * sizeof(Meta);
+}
+
+inline Params make_params(const PagedAttn& a, int ctas) {
+  Params p;
+  p.cu = a.cu;
+  p.ctx = a.ctx;
+  p.table = a.table;
+  p.k = a.c.k;
+  p.v = a.c.v;
+  p.q = a.q;
+  p.q_stride = a.q_stride;
+  p.o = a.o;
+  p.o_stride = a.o_stride;
+  p.lse = a.lse;
+  uint8_t* work = (uint8_t*)a.work;
+  p.part = (float*)work;
+  p.ml = (float2*)(work + part_bytes(ctas, a.c.Dh));
+  p.meta = (Meta*)(work + part_bytes(ctas, a.c.Dh) + ml_bytes(ctas));
+  p.err = a.err;
+  p.W = a.W;
+  p.B = a.B;
+  p.T = a.T;
+  p.H = a.H;
+  p.Hkv = a.c.Hkv;
+  p.G = a.H / a.c.Hkv;
+  p.block = a.block;
+  p.n_pages = a.c.n_pages;
+  p.page_shift = a.c.page_shift;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  return p;
+}
+
+template <typename T, int DH>
+cudaError_t launch_join(const Params& p, int ctas, int rows, cudaStream_t st) {
+  return launch_pdl(paged_join_kernel<T, DH>, dim3(ctas, (rows + kJoinRows - 1) / kJoinRows),
+                    dim3(256), 0, st, p, ctas);
+}
+
+}  // namespace
+
+}  // namespace dlm

@@ -21,7 +21,7 @@ import sys
 import numpy as np
 
 KINDS = ["embed", "qkv_gemm", "qkv_epilogue", "attention", "attn_combine", "wo_gemm",
-         "wo_epilogue", "quantize", "lm_head", "commit", "paged_attention", "paged_join"]
+         "wo_epilogue", "quantize", "lm_head", "commit", "paged_attention"]
 _GEMM = {3: "first stage full", 4: "last stage full", 5: "first accumulator ready",
          6: "last epilogue done"}
 PHASES = {
