@@ -38,8 +38,9 @@ constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P over S), O0, O1 (Dh
 constexpr uint32_t kColO = 256;
 // cost of an item beside its keys, in keys: loading Q, the first S, the epilogue
 constexpr int kItemCost = 128;
-// keys per CTA below which fewer CTAs are used (the join costs more than it saves)
-constexpr int kMinKeys = 256;
+// key tiles of a piece when there is little work (one: the join costs more than
+// the second tile)
+constexpr int kMinTiles = 2;
 // the running reference of a row moves only when its maximum passes it by
 // more than this (log2 units): P stays below 2^8, O is rarely rescaled
 constexpr float kRescaleLog2 = 8.0f;
@@ -121,26 +122,6 @@ __device__ __forceinline__ float fmax3f(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// two float32 in one register pair (sm_100 packed arithmetic)
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // Adds to o (16 columns from c0) the non-finite V elements of keys [k0, k1): the
 // V check set them to zero in shared memory, so that rows that do not see
 // those keys stay clean.
@@ -219,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's range of the work (the scan's scratch is the ring, free until
   // the first load) ----
-  find_range<kThreads>(p, kKeys, kItemCost, kMinKeys, reinterpret_cast<long long*>(ring), sh.start,
+  find_range<kThreads>(p, kKeys, kItemCost, kMinTiles, reinterpret_cast<long long*>(ring), sh.start,
                        sh.stop);
   fence_proxy_async_smem();
   tc_fence_before();
@@ -482,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int quad = warp - kWriter;
       const int row = quad * 32 + lane;
       const uint32_t o_col = tmem + ((uint32_t)(quad * 32) << 16) + kColO;
-      const int rp = row / p.G, rh = row - rp * p.G;   // position and head of the row
+      const int rp = div_g(p, row), rh = row - rp * p.G;   // position and head of the row
       uint32_t eb = 0, done = 0;
       uint32_t no[2] = {0, 0};                         // O accumulations taken
       for (uint32_t n = 0;; ++n) {
@@ -648,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t s_col = lane_addr + i * kKeys;
     const uint32_t o_col = lane_addr + kColO + i * 128;
-    const int rp = row / p.G;                     // position of the row
+    const int rp = div_g(p, row);                     // position of the row
     uint32_t ns = 0;                                  // S tiles taken
     uint32_t nt = 0;                                  // phase of the next turn
     bool ok = true;

@@ -2,72 +2,72 @@
 // (the float32 model; its products would lose half of their bits on the tensor
 // cores).
 //
-// A CTA of 128 threads takes 64 query rows (positions x the G heads of a KV
-// head) and walks its key tiles: S = Q K^T and O += P V as register tiles of 8
-// rows x (BN / 16) keys or (Dh / 16) columns a thread, operands by float4 from
-// shared memory (Q, K, P with the reduction index outermost).  Two or three CTAs
-// per SM hide each other's loads.  Work is cut into equal ranges over all CTAs
-// and joined as in the bf16 kernel, so that a few short sequences still spread
-// over the GPU.  Bound by the FMA pipe and shared memory.
+// A CTA of 256 threads takes 64 query rows (positions x the G heads of a KV
+// head) and walks its key tiles: S = Q K^T and O += P V as register tiles of 4
+// rows x (BN / 16) keys or (Dh / 16) columns a thread, four steps of the
+// reduction at a time from rows in shared memory (8 16-byte loads for 64 FMAs).
+// Q and the K and V tiles come by cp.async, the next tile during this one's
+// arithmetic.  Work is cut into equal ranges over all CTAs and joined as in the
+// bf16 kernel, so that a few short sequences still spread over the GPU.
 #include "paged_attn.cuh"
 
 namespace dlm {
 
 namespace {
 
-constexpr int kRows = 64, kThreads = 128;
-constexpr int kStride = kRows + 4;   // floats between reduction steps of Q and P
+constexpr int kRows = 64, kThreads = 256, kCtasPerSm = 2;
 
 template <int DH>
 struct Shape {
   static constexpr int BN = DH == 128 ? 32 : 64;       // keys per tile
   static constexpr int KN = BN / 16, DN = DH / 16;     // of a thread
-  static constexpr int kCtasPerSm = DH == 128 ? 2 : 3;
-  // shared memory, in floats
+  // floats between rows: 4 more than the row, so that 8 rows' 16-byte loads meet
+  // 32 different banks
+  static constexpr int kLd = DH + 4, kLdP = BN + 4;
+  // shared memory, in floats: Q, two K tiles, two V tiles, P
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + DH * kStride;
-  static constexpr int kV = kK + DH * (BN + 4);
-  static constexpr int kP = kV + BN * DH;
-  static constexpr int kBytes = (kP + BN * kStride) * 4;
+  static constexpr int kK = kQ + kRows * kLd;
+  static constexpr int kV = kK + 2 * BN * kLd;
+  static constexpr int kP = kV + 2 * BN * DH;
+  static constexpr int kBytes = (kP + kRows * kLdP) * 4;
 };
+static_assert(kCtasPerSm * (Shape<128>::kBytes + 2048) <= 227 * 1024 &&
+                  kCtasPerSm * (Shape<64>::kBytes + 2048) <= 227 * 1024,
+              "two CTAs per SM");
 
-// N consecutive floats of shared memory
+// four floats of shared memory, as two pairs
+__device__ __forceinline__ ulonglong2 lds4(const float* p) {
+  return *reinterpret_cast<const ulonglong2*>(p);
+}
+
+// 16 bytes into shared memory, zeros if !live
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
-__device__ __forceinline__ void lds(const float* p, float (&v)[N]) {
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p + i);
-      v[i] = x.x;
-      v[i + 1] = x.y;
-      v[i + 2] = x.z;
-      v[i + 3] = x.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(p + i);
-      v[i] = x.x;
-      v[i + 1] = x.y;
-    }
-  }
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int DH>
-__global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_f32_kernel(const Params p) {
   using SH = Shape<DH>;
   constexpr int BN = SH::BN, KN = SH::KN, DN = SH::DN;
   extern __shared__ __align__(16) float sm[];
-  float* qs = sm + SH::kQ;   // [DH][kStride]
-  float* ks = sm + SH::kK;   // [DH][BN + 4]
-  float* vs = sm + SH::kV;   // [BN][DH]
-  float* ps = sm + SH::kP;   // [BN][kStride]
+  constexpr int kLd = SH::kLd, kLdP = SH::kLdP;
+  float* qs = sm + SH::kQ;   // [kRows][kLd]
+  float* ks = sm + SH::kK;   // [2][BN][kLd]
+  float* vs = sm + SH::kV;   // [2][BN][DH]
+  float* ps = sm + SH::kP;   // [kRows][kLdP]
   __shared__ int start[4], stop[4];
-  __shared__ long long scan[kThreads / 32];
+  __shared__ long long scan[2 * kThreads / 32];
   __shared__ Item item;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int ty = tid >> 4, tx = tid & 15;   // rows 8 ty .., keys KN tx .., columns DN tx ..
-  find_range<kThreads>(p, BN, BN, 2 * BN, scan, start, stop);
+  const int ty = tid >> 4, tx = tid & 15;   // rows 4 ty .., keys tx + 16 j, columns DN tx ..
+  find_range<kThreads>(p, BN, BN, 1, scan, start, stop);
   __syncthreads();
   Walker walk(start, stop);
   const float* kc = (const float*)p.k;
@@ -86,95 +86,99 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const Params p
     // G > 64: the item's single position in two passes
     for (int r0 = 0; r0 < rows; r0 += kRows) {
       // this thread's rows: what they see
-      int lim[8];
+      int lim[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + ty * 8 + i;
-        lim[i] = r < rows ? visible(it.pos0 + r / p.G, it.ctx, p.block) : 0;
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + ty * 4 + i;
+        lim[i] = r < rows ? visible(it.pos0 + div_g(p, r), it.ctx, p.block) : 0;
       }
-      __syncthreads();
-      // Q, transposed: a lane's row, 4 columns at a time
-      for (int x = warp; x < DH / 4 * (kRows / 32); x += kThreads / 32) {
-        const int lr = (x % (kRows / 32)) * 32 + lane, c = x / (kRows / 32) * 4;
-        const int r = r0 + lr;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
-          const int pos = r / p.G, h = it.g * p.G + r - pos * p.G;
-          v = __ldg(reinterpret_cast<const float4*>((const float*)p.q + (it.row0 + pos) * p.q_stride +
-                                                    (int64_t)h * DH + c));
+      __syncthreads();   // the rows before these are done with Q, K, V and P
+#pragma unroll 4
+      for (int x = tid; x < kRows * DH / 4; x += kThreads) {
+        const int lr = x / (DH / 4), c = x % (DH / 4) * 4, r = r0 + lr;
+        const int pos = div_g(p, r), h = it.g * p.G + r - pos * p.G;
+        const bool live = r < rows;
+        copy16(qs + lr * kLd + c,
+               (const float*)p.q + (live ? (it.row0 + pos) * p.q_stride + (int64_t)h * DH + c : 0), live);
+      }
+      // K and V of tile t into buffer t & 1; keys behind the sequence are zero
+      auto load = [&](int t) {
+        float* kd = ks + (t & 1) * BN * kLd;
+        float* vd = vs + (t & 1) * BN * DH;
+#pragma unroll 4
+        for (int x = tid; x < BN * DH / 4; x += kThreads) {
+          const int j = x / (DH / 4), c = x % (DH / 4) * 4, k = t * BN + j;
+          bool live = k < it.ctx;
+          int64_t at = 0;
+          if (live) {
+            const int page = __ldg(p.table + (size_t)it.b * p.W + (k >> p.page_shift));
+            live = page >= 0 && page < p.n_pages;
+            if (live)
+              at = ((((int64_t)page * p.Hkv + it.g) << p.page_shift) + (k & page_mask)) * DH + c;
+            else
+              raise_error(p.err, DLM_EBOUNDS);
+          }
+          copy16(kd + j * kLd + c, kc + at, live);
+          copy16(vd + j * DH + c, vc + at, live);
         }
-        qs[(c + 0) * kStride + lr] = v.x;
-        qs[(c + 1) * kStride + lr] = v.y;
-        qs[(c + 2) * kStride + lr] = v.z;
-        qs[(c + 3) * kStride + lr] = v.w;
-      }
-      float m[8], l[8], acc[8][DN];
+        copy_commit();
+      };
+      if (it.ts < it.te) load(it.ts);
+      float m[4], l[4];
+      uint64_t acc[4][DN / 2];   // pairs of columns
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         m[i] = -CUDART_INF_F;
         l[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < DN; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < DN / 2; ++j) acc[i][j] = 0;
       }
       for (int t = it.ts; t < it.te; ++t) {
         const int k0 = t * BN;
-        __syncthreads();   // the previous tile is done with
-        auto row_of = [&](int j) -> int64_t {   // of key k0 + j in the cache, or -1
-          const int k = k0 + j;
-          if (k >= it.ctx) return -1;
-          const int page = __ldg(p.table + (size_t)it.b * p.W + (k >> p.page_shift));
-          if (page < 0 || page >= p.n_pages) {
-            raise_error(p.err, DLM_EBOUNDS);
-            return -1;
-          }
-          return (((int64_t)page * p.Hkv + it.g) << p.page_shift) + (k & page_mask);
-        };
-        {
-          // K, transposed (a lane's key); keys behind the sequence are zero
-          constexpr int kParts = kThreads / BN;
-          const int j = tid % BN;
-          const int64_t row = row_of(j);
-          const float4* src = reinterpret_cast<const float4*>(kc + row * DH);
-#pragma unroll 8
-          for (int c = tid / BN; c < DH / 4; c += kParts) {
-            const float4 v = row >= 0 ? __ldg(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-            ks[(c * 4 + 0) * (BN + 4) + j] = v.x;
-            ks[(c * 4 + 1) * (BN + 4) + j] = v.y;
-            ks[(c * 4 + 2) * (BN + 4) + j] = v.z;
-            ks[(c * 4 + 3) * (BN + 4) + j] = v.w;
-          }
-        }
-#pragma unroll 4
-        for (int x = tid; x < BN * DH / 4; x += kThreads) {
-          const int64_t row = row_of(x / (DH / 4));
-          reinterpret_cast<float4*>(vs)[x] =
-              row >= 0 ? __ldg(reinterpret_cast<const float4*>(vc + row * DH) + x % (DH / 4))
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t + 1 < it.te) {
+          load(t + 1);
+          copy_wait<1>();
+        } else {
+          copy_wait<0>();
         }
         __syncthreads();
         // S = Q K^T
-        float s[8][KN];
+        // (packed pairs: the even and the odd columns' sums)
+        uint64_t s2[4][KN];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < KN; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-        for (int d = 0; d < DH; ++d) {
-          float a[8], b[KN];
-          lds<8>(qs + d * kStride + ty * 8, a);
-          lds<KN>(ks + d * (BN + 4) + tx * KN, b);
+          for (int j = 0; j < KN; ++j) s2[i][j] = 0;
+        const float* kt = ks + (t & 1) * BN * kLd;
+        const float* vt = vs + (t & 1) * BN * DH;
+#pragma unroll 2
+        for (int d = 0; d < DH; d += 4) {
+          ulonglong2 b[KN];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int j = 0; j < KN; ++j) b[j] = lds4(kt + (tx + 16 * j) * kLd + d);
 #pragma unroll
-            for (int j = 0; j < KN; ++j) s[i][j] = fmaf(a[i], b[j], s[i][j]);
+          for (int i = 0; i < 4; ++i) {
+            const ulonglong2 a = lds4(qs + (ty * 4 + i) * kLd + d);
+#pragma unroll
+            for (int j = 0; j < KN; ++j) s2[i][j] = fma2(a.y, b[j].y, fma2(a.x, b[j].x, s2[i][j]));
+          }
         }
+        float s[4][KN];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < KN; ++j) {
+            float even, odd;
+            unpack2(s2[i][j], even, odd);
+            s[i][j] = even + odd;
+          }
         // softmax: a row's 16 threads are 16 lanes of a warp
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           float mx = -CUDART_INF_F;
 #pragma unroll
           for (int j = 0; j < KN; ++j) {
-            s[i][j] = k0 + tx * KN + j < lim[i] ? s[i][j] * p.scale_log2 : -CUDART_INF_F;
+            s[i][j] = k0 + tx + 16 * j < lim[i] ? s[i][j] * p.scale_log2 : -CUDART_INF_F;
             mx = fmaxf(mx, s[i][j]);
           }
 #pragma unroll
@@ -191,51 +195,67 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const Params p
           }
           l[i] = l[i] * alpha + sum;   // this thread's keys; added up at the end
 #pragma unroll
-          for (int j = 0; j < DN; ++j) acc[i][j] *= alpha;
+          for (int j = 0; j < DN / 2; ++j) acc[i][j] = mul2(acc[i][j], pack2(alpha, alpha));
         }
 #pragma unroll
-        for (int j = 0; j < KN; ++j) {
-          float* dst = ps + (tx * KN + j) * kStride + ty * 8;
-          *reinterpret_cast<float4*>(dst) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-          *reinterpret_cast<float4*>(dst + 4) = make_float4(s[4][j], s[5][j], s[6][j], s[7][j]);
-        }
-        __syncthreads();
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < KN; ++j) ps[(ty * 4 + i) * kLdP + tx + 16 * j] = s[i][j];
+        __syncwarp();   // a row's P is written and read by one half-warp
         // O += P V; in tiles with hidden keys a probability of 0 takes nothing
         // from V (0 x infinity would be NaN)
         auto pv = [&](auto hidden) {
-#pragma unroll 4
-          for (int k = 0; k < BN; ++k) {
-            float a[8], b[DN];
-            lds<8>(ps + k * kStride + ty * 8, a);
-            lds<DN>(vs + k * DH + tx * DN, b);
+#pragma unroll 2
+          for (int k = 0; k < BN; k += 4) {
+            uint64_t b[4][DN / 2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int y = 0; y < 4; ++y) {
+              const float* src = vt + (k + y) * DH + tx * DN;
+              if constexpr (DN == 2) {
+                b[y][0] = *reinterpret_cast<const uint64_t*>(src);
+              } else {
 #pragma unroll
-              for (int j = 0; j < DN; ++j)
-                acc[i][j] = fmaf(a[i], decltype(hidden)::value && a[i] == 0.f ? 0.f : b[j], acc[i][j]);
+                for (int j = 0; j < DN / 2; j += 2) {
+                  const ulonglong2 v = lds4(src + 2 * j);
+                  b[y][j] = v.x;
+                  b[y][j + 1] = v.y;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 a = *reinterpret_cast<const float4*>(ps + (ty * 4 + i) * kLdP + k);
+              const float w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int j = 0; j < DN / 2; ++j)
+                  acc[i][j] = fma2(pack2(w[y], w[y]),
+                                   decltype(hidden)::value && w[y] == 0.f ? 0ull : b[y][j], acc[i][j]);
+            }
           }
         };
         if (k0 + BN > it.fix)
           pv(std::true_type{});
         else
           pv(std::false_type{});
+        __syncthreads();   // this buffer is loaded again
       }
       // results
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-        const int r = r0 + ty * 8 + i;
+        const int r = r0 + ty * 4 + i;
         if (r >= rows) continue;
-        const int pos = r / p.G, h = it.g * p.G + r - pos * p.G;
+        const int pos = div_g(p, r), h = it.g * p.G + r - pos * p.G;
         const int64_t grow = (int64_t)it.row0 + pos;
         const size_t prow = ((size_t)blockIdx.x * 2 + it.slot) * kSlotRows + r;
         const float inv = !it.whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
         float* dst = it.whole ? (float*)p.o + grow * p.o_stride + (int64_t)h * DH : p.part + prow * DH;
 #pragma unroll
-        for (int j = 0; j < DN; j += 2)
-          *reinterpret_cast<float2*>(dst + tx * DN + j) =
-              make_float2(acc[i][j] * inv, acc[i][j + 1] * inv);
+        for (int j = 0; j < DN / 2; ++j)
+          *reinterpret_cast<uint64_t*>(dst + tx * DN + 2 * j) = mul2(acc[i][j], pack2(inv, inv));
         if (tx == 0) {
           if (!it.whole)
             p.ml[prow] = make_float2(m[i], l[i]);
@@ -258,7 +278,7 @@ cudaError_t launch(const PagedAttn& a, int num_sms, cudaStream_t st) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DH>::kBytes);
   });
   if (e != cudaSuccess) return e;
-  const int ctas = num_sms * Shape<DH>::kCtasPerSm;
+  const int ctas = num_sms * kCtasPerSm;
   Params p = make_params(a, ctas);
   p.npos = p.G < kRows ? kRows / p.G : 1;
   p.positions = p.npos;
@@ -270,7 +290,7 @@ cudaError_t launch(const PagedAttn& a, int num_sms, cudaStream_t st) {
 }  // namespace
 
 size_t paged_attention_f32_work(int Dh, int num_sms) {
-  return work_bytes(num_sms * (Dh == 128 ? Shape<128>::kCtasPerSm : Shape<64>::kCtasPerSm), Dh);
+  return work_bytes(num_sms * kCtasPerSm, Dh);
 }
 
 cudaError_t paged_attention_f32(const PagedAttn& a, int num_sms, cudaStream_t st) {

@@ -15,6 +15,31 @@ namespace {
 
 constexpr int kSlotRows = 256;   // rows of a partial in the workspace
 
+// two float32 in one register pair (sm_100 packed arithmetic)
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // A piece of work: up to `positions` consecutive positions of a sequence for one
 // KV head (with that head's G query heads), and a range of their key tiles.
 struct Item {
@@ -58,6 +83,8 @@ struct Params {
   int* err;
   int W, B, T, H, Hkv, G, npos, block, n_pages, page_shift;
   int positions;       // of an item: npos, or 2 * npos (two row tiles)
+  uint32_t g_inv;      // ceil(2^16 / G): x / G for x < 256
+  double inv_grid;     // 1 / CTAs
   float scale_log2;
 };
 
@@ -99,72 +126,145 @@ struct SeqCost {
   }
 };
 
+// x / G for 0 <= x < 256, G <= 128: the rounded-up factor adds less than
+// 2^8 / 2^16 to the quotient, and its fraction is at most 1 - 2^-7
+__device__ __forceinline__ int div_g(const Params& p, int x) {
+  return (int)(((uint32_t)x * p.g_inv) >> 16);
+}
+
 __device__ __forceinline__ bool seq_ok(const Params& p, int c0, int c1, int ctx) {
   return c0 >= 0 && c0 <= c1 && c1 <= p.T && ctx >= 0 &&
          (long long)ctx <= ((long long)p.W << p.page_shift);
 }
 
-// This CTA's range of the work, as (KV head, sequence, item, key tile): all items,
-// KV head by KV head, laid end to end in units of cost and cut into equal
-// shares (of at least min_keys).  A scan over the sequences' costs, consecutive
-// ones per thread; the owners of the range's two ends turn them into an item
-// and a tile.  `scan`: shared memory, a number per warp.  The caller
-// synchronises before it reads start and stop ([0] = Hkv: the end).
+// The block's exclusive scan of x; *total its sum.  `scan`: shared memory, a
+// number per warp.
 template <int THREADS>
-__device__ void find_range(const Params& p, int key_tile, int item_cost, int min_keys,
-                           long long* scan, int* start, int* stop) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int pp = p.positions;
-  const int per = (p.B + THREADS - 1) / THREADS;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), ctx = __ldg(p.ctx + b);
-    if (!seq_ok(p, c0, c1, ctx)) {
-      if (blockIdx.x == 0) raise_error(p.err, DLM_EBOUNDS);
-      continue;
-    }
-    const SeqCost s(c1 - c0, ctx, pp, p.block, item_cost);
-    mine += s.cum(s.items);
-  }
-  long long incl = mine;
+__device__ __forceinline__ long long block_scan(long long x, long long* scan, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long o = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += o;
   }
   if (lane == 31) scan[warp] = incl;
-  if (tid < 4) start[tid] = stop[tid] = 0;
   __syncthreads();
-  long long before = 0, w1 = 0;
+  long long before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    if (w == warp) before = w1;
-    w1 += scan[w];
+    if (w == warp) before = all;
+    all += scan[w];
   }
-  const long long first = before + incl - mine;   // cost before sequence b0
+  *total = all;
+  return before + incl - x;
+}
+
+// u / w, by a double's quotient and a correction (u < 2^53)
+__device__ __forceinline__ int small_quotient(long long u, long long w) {
+  int g = (int)((double)u * __drcp_rn((double)w));
+  g -= g * w > u;
+  g += (g + 1) * w <= u;
+  return g;
+}
+
+// This CTA's range of the work, as (KV head, sequence, item, key tile) in start
+// and stop ([0] = Hkv: the end).  A scan over the sequences, consecutive ones per
+// thread; the owners of the range's two ends turn them into an item and a tile.
+//   Little work (every item cut into pieces of min_tiles key tiles gives no more
+//   pieces than CTAs): a piece per CTA, so that none has two items.
+//   Else all items, KV head by KV head, are laid end to end in units of cost
+//   and cut into equal shares.
+// `scan`: shared memory, two numbers per warp.  The caller synchronises before
+// it reads start and stop.
+template <int THREADS>
+__device__ void find_range(const Params& p, int key_tile, int item_cost, int min_tiles,
+                           long long* scan, int* start, int* stop) {
+  const int tid = threadIdx.x;
+  const int pp = p.positions;
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  // the sequence's new tokens and length; none if the input is bad
+  auto sequence = [&](int b, int& n, int& ctx, bool report) {
+    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+    ctx = __ldg(p.ctx + b);
+    n = c1 - c0;
+    if (!seq_ok(p, c0, c1, ctx)) {
+      if (report) raise_error(p.err, DLM_EBOUNDS);
+      n = ctx = 0;
+    }
+  };
+  // key tiles of item j of a sequence
+  auto tiles = [&](int n, int ctx, int j) {
+    const int i1 = min(n, (j + 1) * pp);
+    return (visible(ctx - n + i1 - 1, ctx, p.block) + key_tile - 1) / key_tile;
+  };
+  if (tid < 4) start[tid] = stop[tid] = 0;
+  long long mine = 0, w1;
+  for (int b = b0; b < b1; ++b) {
+    int n, ctx;
+    sequence(b, n, ctx, blockIdx.x == 0);
+    const SeqCost s(n, ctx, pp, p.block, item_cost);
+    mine += s.cum(s.items);
+  }
+  long long first = block_scan<THREADS>(mine, scan, &w1);
   const long long total = w1 * p.Hkv;
-  // (doubles: every CTA computes the same edges, and no 64-bit divisions)
-  const int ctas = (int)max(1.0, min((double)gridDim.x, floor((double)total * (1.0 / min_keys))));
-  const double share = (double)total / ctas;
-  auto edge = [&](int k) { return k >= ctas ? total : min(total, (long long)(share * k)); };
-  const long long u[2] = {edge(blockIdx.x), edge(blockIdx.x + 1)};
+  if (total <= (long long)gridDim.x * (min_tiles * key_tile + item_cost)) {
+    auto pieces = [&](int n, int ctx, int j) {
+      return max(1, (tiles(n, ctx, j) + min_tiles - 1) / min_tiles);
+    };
+    long long own = 0, all;
+    for (int b = b0; b < b1; ++b) {
+      int n, ctx;
+      sequence(b, n, ctx, false);
+      for (int j = 0; j * pp < n; ++j) own += pieces(n, ctx, j);
+    }
+    const long long before = block_scan<THREADS>(own, scan + THREADS / 32, &all);
+    if (all * p.Hkv <= gridDim.x) {
+      if ((int)blockIdx.x >= all * p.Hkv) {
+        if (tid == 0) start[0] = stop[0] = p.Hkv;
+        return;
+      }
+      const int g = (int)blockIdx.x / (int)all;
+      int r = (int)blockIdx.x - g * (int)all - (int)before;
+      if (r < 0 || r >= own) return;
+      for (int b = b0; b < b1; ++b) {
+        int n, ctx;
+        sequence(b, n, ctx, false);
+        for (int j = 0; j * pp < n; ++j) {
+          const int k = pieces(n, ctx, j);
+          if (r < k) {
+            start[0] = stop[0] = g;
+            start[1] = stop[1] = b;
+            start[2] = j;
+            start[3] = r * min_tiles;
+            stop[2] = r + 1 < k ? j : j + 1;
+            stop[3] = r + 1 < k ? (r + 1) * min_tiles : 0;
+            return;
+          }
+          r -= k;
+        }
+      }
+      return;
+    }
+  }
+  // (a share rounded up: the last CTAs may have none)
+  const long long share = (long long)((double)total * p.inv_grid) + 1;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     int* dst = e == 0 ? start : stop;
-    if (w1 == 0 || u[e] >= total) {
+    const long long u = min(total, share * ((int)blockIdx.x + e));
+    if (u >= total) {
       if (tid == 0) dst[0] = p.Hkv;   // the end
       continue;
     }
-    int g = (int)((double)u[e] / (double)w1);   // the quotient, or one off it
-    g -= g * w1 > u[e];
-    g += (g + 1) * w1 <= u[e];
-    long long r = u[e] - g * w1 - first;
+    const int g = small_quotient(u, w1);
+    long long r = u - g * w1 - first;
     if (r < 0 || r >= mine) continue;
     for (int b = b0; b < b1; ++b) {
-      const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), ctx = __ldg(p.ctx + b);
-      if (!seq_ok(p, c0, c1, ctx)) continue;
-      const SeqCost s(c1 - c0, ctx, pp, p.block, item_cost);
+      int n, ctx;
+      sequence(b, n, ctx, false);
+      const SeqCost s(n, ctx, pp, p.block, item_cost);
       const long long c = s.cum(s.items);
       if (r >= c) {
         r -= c;
@@ -178,14 +278,14 @@ __device__ void find_range(const Params& p, int key_tile, int item_cost, int min
         else
           hi = mid;
       }
-      const long long at = r - s.cum(lo), cost = s.cum(lo + 1) - s.cum(lo);
-      const int i1 = (int)min((long long)s.n, (long long)(lo + 1) * pp);
-      const int kt = (visible(ctx - s.n + i1 - 1, ctx, p.block) + key_tile - 1) / key_tile;
+      // the share of the item's cost, as key tiles: < kt; 0: the item starts in
+      // the range behind this edge
+      const float at = (float)(r - s.cum(lo)), cost = (float)(s.cum(lo + 1) - s.cum(lo));
+      const int kt = tiles(n, ctx, lo);
       dst[0] = g;
       dst[1] = b;
       dst[2] = lo;
-      // < kt; 0: the item starts in this range
-      dst[3] = max(0, min(kt - 1, (int)((double)at * kt / (double)cost)));
+      dst[3] = max(0, min(kt - 1, (int)__fdividef(at * kt, cost)));
       break;
     }
   }
@@ -363,7 +463,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_c
   for (int u = 0; u < R; ++u) {
     if (r0 + 8 * u >= used) continue;
     const int x = r0 + 8 * u - tile * kTileRows;
-    const int rp = x / p.G, rh = x - rp * p.G, pos = tile * p.npos + rp;
+    const int rp = div_g(p, x), rh = x - rp * p.G, pos = tile * p.npos + rp;
     const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
     const int64_t grow = (int64_t)me.row0 + pos;
     const int head = me.g * p.G + rh;
@@ -417,6 +517,8 @@ inline Params make_params(const PagedAttn& a, int ctas) {
   p.block = a.block;
   p.n_pages = a.c.n_pages;
   p.page_shift = a.c.page_shift;
+  p.g_inv = (65536u + (uint32_t)p.G - 1u) / (uint32_t)p.G;
+  p.inv_grid = 1.0 / ctas;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   return p;
 }
