@@ -29,6 +29,7 @@ namespace cg = cooperative_groups;
 // ---------------------------------------------------------------------------
 constexpr int kResizeThreads = 1024;
 constexpr int kResizeSeqs = kPagedMaxBatch;
+constexpr int kRun = 4;   // consecutive slots of a thread: mostly one sequence and page
 
 struct Scan3 {
   long long need, gone, tok;
@@ -39,6 +40,11 @@ __device__ __forceinline__ Scan3 operator+(const Scan3& a, const Scan3& b) {
 __device__ __forceinline__ Scan3 shfl_up3(const Scan3& a, int d) {
   return Scan3{__shfl_up_sync(0xffffffffu, a.need, d), __shfl_up_sync(0xffffffffu, a.gone, d),
                __shfl_up_sync(0xffffffffu, a.tok, d)};
+}
+
+__device__ __forceinline__ Scan3 shfl3(const Scan3& a, int lane) {
+  return Scan3{__shfl_sync(0xffffffffu, a.need, lane), __shfl_sync(0xffffffffu, a.gone, lane),
+               __shfl_sync(0xffffffffu, a.tok, lane)};
 }
 
 // largest i in [0, n) with first[i] <= x, for ascending first, first[0] <= x
@@ -63,7 +69,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
   int* s_tok = s_gone + a.B;     // [B] T: new tokens before this sequence's, capped at max_new
   int* s_ok = s_tok + a.B;       // [B] served
   __shared__ Scan3 warp_sum[32];
-  __shared__ long long s_total[3];   // pages taken, pages released, tokens
+  __shared__ unsigned long long s_taken;   // pages taken
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x, n_ranks = gridDim.x;
@@ -93,22 +99,27 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
     s_new[b] = want;
     mine = mine + change(cur, want);
   }
-  Scan3 incl = mine;
+  auto warp_scan = [&](Scan3 x) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const Scan3 o = shfl_up3(incl, d);
-    if (lane >= d) incl = incl + o;
-  }
+    for (int d = 1; d < 32; d <<= 1) {
+      const Scan3 o = shfl_up3(x, d);
+      if (lane >= d) x = x + o;
+    }
+    return x;
+  };
+  const Scan3 incl = warp_scan(mine);
   if (lane == 31) warp_sum[warp] = incl;
-  if (tid < 3) s_total[tid] = 0;
+  if (tid == 0) s_taken = 0;
   __syncthreads();
-  Scan3 before{0, 0, 0}, all{0, 0, 0};
-  for (int w = 0; w < kResizeThreads / 32; ++w) {
-    if (w == warp) before = all;
-    all = all + warp_sum[w];
-  }
-  Scan3 at = Scan3{before.need + incl.need - mine.need, before.gone + incl.gone - mine.gone,
-                   before.tok + incl.tok - mine.tok};
+  // every warp scans the warps' sums
+  static_assert(kResizeThreads == 1024, "a lane per warp");
+  const Scan3 sums = warp_scan(warp_sum[lane]);
+  const Scan3 all = shfl3(sums, 31), upto = shfl3(sums, warp);
+  // before this thread's sequences
+  const Scan3 own = warp_sum[warp];
+  Scan3 at = Scan3{upto.need - own.need + incl.need - mine.need,
+                   upto.gone - own.gone + incl.gone - mine.gone,
+                   upto.tok - own.tok + incl.tok - mine.tok};
   // a broken stack: nothing changes
   const bool broken = n_free < 0 || n_free > a.n_pages || n_free + all.gone > a.n_pages;
   const long long have = broken ? 0 : n_free + all.gone;
@@ -130,13 +141,13 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
   for (int d = 16; d > 0; d >>= 1) taken += __shfl_xor_sync(0xffffffffu, taken, d);
   // whole numbers: the order of the additions does not matter
   if (lane == 0 && taken > 0)
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s_total[0]), (unsigned long long)taken);
+    atomicAdd(&s_taken, (unsigned long long)taken);
   __syncthreads();
   // every CTA has read the lengths and the stack's height
   if (n_ranks > 1) cg::this_cluster().sync();
 
   const int F = broken ? 0 : (int)all.gone;
-  const int K = (int)s_total[0];
+  const int K = (int)s_taken;
   const int n_tok = (int)min(all.tok, (long long)a.max_new);
   // page id j of the released ones, and the k-th popped one
   auto checked = [&](int page) {
@@ -150,40 +161,66 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
   auto popped = [&](int k) {
     return k < F ? released(k) : checked(a.free_pages[n_free + F - 1 - k]);
   };
-  const int first = rank * kResizeThreads + tid, step = n_ranks * kResizeThreads;
+  // outputs, as one list of tasks over the cluster's threads (neighbours go to
+  // different CTAs), so that their chains of loads run side by side
+  const int first = tid * n_ranks + rank, step = n_ranks * kResizeThreads;
   if (first == 0) {
     if (broken) raise_error(a.err, DLM_EBOUNDS);
     *a.n_free_out = broken ? n_free : n_free + F - K;
     a.cu[0] = 0;
   }
-  for (int b = first; b < a.B; b += step) {
+  const int kept = max(0, F - K);                      // released pages that stay on the stack
+  const int runs = (a.max_new + kRun - 1) / kRun;      // of the slot map
+  const long long tasks = (long long)a.B + K + kept + runs;
+  for (long long x = first; x < tasks; x += step) {
+    long long y = x;
+    if (y < runs) {
+      // a slot per new token
+      const int t0 = (int)y * kRun;
+      int b = -1, col = -1;
+      int64_t base = -1;
+#pragma unroll 1
+      for (int t = t0; t < min(t0 + kRun, a.max_new); ++t) {
+        int64_t slot = -1;
+        if (t < n_tok) {
+          if (b < 0 || (b + 1 < a.B && t >= s_tok[b + 1])) {   // another sequence
+            b = find_last(s_tok, a.B, t);
+            col = -1;
+          }
+          if (s_ok[b]) {
+            const int cur = s_cur[b];
+            const int pos = cur + (t - s_tok[b]);
+            if (pos >> sh != col) {                            // another page
+              col = pos >> sh;
+              const int pc = pages(cur);
+              const int page = col < pc ? checked(a.table[(size_t)b * a.W + col])
+                                        : popped(s_need[b] + (col - pc));
+              base = page >= 0 && page < a.n_pages ? (int64_t)page << sh : -1;
+            }
+            if (base >= 0) slot = base + (pos & (int)page_mask);
+          }
+        }
+        a.slots[t] = slot;
+      }
+      continue;
+    }
+    y -= runs;
+    if (y < K) {
+      // a new page into its table (served sequences that need pages are the first
+      // of those that need any, so page k's owner is found in D)
+      const int k = (int)y, b = find_last(s_need, a.B, k);
+      a.table[(size_t)b * a.W + pages(s_cur[b]) + (k - s_need[b])] = popped(k);
+      continue;
+    }
+    y -= K;
+    if (y < kept) {
+      // position n_free + y of the stack
+      a.free_pages[n_free + (int)y] = released(F - 1 - (int)y);
+      continue;
+    }
+    const int b = (int)(y - kept);
     a.out_lens[b] = s_ok[b] ? s_new[b] : s_cur[b];
     a.cu[b + 1] = b + 1 < a.B ? s_tok[b + 1] : n_tok;
-  }
-  // new pages into the tables (served sequences that need pages are the
-  // first of those that need any, so page k's owner is found in D)
-  for (int k = first; k < K; k += step) {
-    const int b = find_last(s_need, a.B, k);
-    a.table[(size_t)b * a.W + pages(s_cur[b]) + (k - s_need[b])] = popped(k);
-  }
-  // released pages that stay on the stack
-  for (int pos = n_free + first; pos < n_free + F - K; pos += step)
-    a.free_pages[pos] = released(F - 1 - (pos - n_free));
-  // a slot per new token
-  for (int t = first; t < a.max_new; t += step) {
-    int64_t slot = -1;
-    if (t < n_tok) {
-      const int b = find_last(s_tok, a.B, t);
-      if (s_ok[b]) {
-        const int cur = s_cur[b];
-        const int pos = cur + (t - s_tok[b]);
-        const int col = pos >> sh, pc = pages(cur);
-        const int page = col < pc ? checked(a.table[(size_t)b * a.W + col])
-                                  : popped(s_need[b] + (col - pc));
-        if (page >= 0 && page < a.n_pages) slot = ((int64_t)page << sh) + (pos & (int)page_mask);
-      }
-    }
-    a.slots[t] = slot;
   }
 }
 
@@ -225,9 +262,9 @@ cudaError_t paged_resize(const PagedResize& a, cudaStream_t st) {
                                 6 * kResizeSeqs * (int)sizeof(int));
   });
   if (e != cudaSuccess) return e;
-  // one CTA up to two outputs a thread, then a cluster of up to 8
+  // one CTA up to a run of slots a thread, then a cluster of up to 8
   int ranks = 1;
-  while (ranks < 8 && (long long)ranks * 2 * kResizeThreads < a.max_new) ranks *= 2;
+  while (ranks < 8 && (long long)ranks * kRun * kResizeThreads < a.max_new) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);
   cfg.blockDim = dim3(kResizeThreads);
