@@ -161,9 +161,9 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
   auto popped = [&](int k) {
     return k < F ? released(k) : checked(a.free_pages[n_free + F - 1 - k]);
   };
-  // outputs, as one list of tasks over the cluster's threads (neighbours go to
-  // different CTAs), so that their chains of loads run side by side
-  const int first = tid * n_ranks + rank, step = n_ranks * kResizeThreads;
+  // outputs, as one list of tasks over the cluster's threads (neighbouring warps'
+  // go to different CTAs), so that their chains of loads run side by side
+  const int first = (warp * n_ranks + rank) * 32 + lane, step = n_ranks * kResizeThreads;
   if (first == 0) {
     if (broken) raise_error(a.err, DLM_EBOUNDS);
     *a.n_free_out = broken ? n_free : n_free + F - K;
@@ -175,32 +175,44 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
   for (long long x = first; x < tasks; x += step) {
     long long y = x;
     if (y < runs) {
-      // a slot per new token
+      // a slot per new token; a run's sequence and page are looked up when they change
       const int t0 = (int)y * kRun;
-      int b = -1, col = -1;
+      int64_t slot[kRun];
+      int b = -1, end = t0, col = -1, cur = 0, tb = 0, page_b = 0;
+      bool ok = false;
       int64_t base = -1;
-#pragma unroll 1
-      for (int t = t0; t < min(t0 + kRun, a.max_new); ++t) {
-        int64_t slot = -1;
-        if (t < n_tok) {
-          if (b < 0 || (b + 1 < a.B && t >= s_tok[b + 1])) {   // another sequence
-            b = find_last(s_tok, a.B, t);
-            col = -1;
-          }
-          if (s_ok[b]) {
-            const int cur = s_cur[b];
-            const int pos = cur + (t - s_tok[b]);
-            if (pos >> sh != col) {                            // another page
-              col = pos >> sh;
-              const int pc = pages(cur);
-              const int page = col < pc ? checked(a.table[(size_t)b * a.W + col])
-                                        : popped(s_need[b] + (col - pc));
-              base = page >= 0 && page < a.n_pages ? (int64_t)page << sh : -1;
-            }
-            if (base >= 0) slot = base + (pos & (int)page_mask);
-          }
+#pragma unroll
+      for (int u = 0; u < kRun; ++u) {
+        const int t = t0 + u;
+        slot[u] = -1;
+        if (t >= n_tok) continue;
+        if (t >= end) {
+          b = find_last(s_tok, a.B, t);
+          end = b + 1 < a.B ? s_tok[b + 1] : n_tok;
+          ok = s_ok[b] != 0;
+          cur = s_cur[b];
+          tb = s_tok[b];
+          page_b = s_need[b] - pages(cur);
+          col = -1;
         }
-        a.slots[t] = slot;
+        if (!ok) continue;
+        const int pos = cur + (t - tb);
+        if (pos >> sh != col) {
+          col = pos >> sh;
+          const int page = col < pages(cur) ? checked(a.table[(size_t)b * a.W + col])
+                                            : popped(page_b + col);
+          base = page >= 0 && page < a.n_pages ? (int64_t)page << sh : -1;
+        }
+        if (base >= 0) slot[u] = base + (pos & (int)page_mask);
+      }
+      if (t0 + kRun <= a.max_new && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
+        longlong2* dst = reinterpret_cast<longlong2*>(a.slots + t0);
+        dst[0] = make_longlong2(slot[0], slot[1]);
+        dst[1] = make_longlong2(slot[2], slot[3]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kRun; ++u)
+          if (t0 + u < a.max_new) a.slots[t0 + u] = slot[u];
       }
       continue;
     }
