@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
   const int rank = blockIdx.x, n_ranks = gridDim.x;
   const int sh = a.page_shift;
   const long long page_mask = (1ll << sh) - 1;
+  pdl_wait_then_release();
   const int n_free = *a.n_free_in;
   auto pages = [&](int n) { return (int)(((long long)n + page_mask) >> sh); };
 
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const PagedKV c, const ui
                                                        int64_t k_stride, int64_t v_stride,
                                                        const int64_t* __restrict__ slots, int n,
                                                        int* err) {
+  pdl_wait_then_release();
   const int head_chunks = c.Dh * c.esize / 16;
   const int row_chunks = c.Hkv * head_chunks;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -282,13 +284,15 @@ cudaError_t paged_resize(const PagedResize& a, cudaStream_t st) {
   cfg.blockDim = dim3(kResizeThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ranks;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, resize_kernel, a);
 }
 
@@ -296,10 +300,9 @@ cudaError_t paged_kv_write(const PagedKV& c, const void* k, const void* v, int64
                            int64_t v_stride, const int64_t* slots, int n, int* err,
                            cudaStream_t st) {
   const int64_t pieces = (int64_t)n * c.Hkv * (c.Dh * c.esize / 16);
-  kv_write_kernel<<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(
-      c, (const uint8_t*)k, (const uint8_t*)v, k_stride * c.esize, v_stride * c.esize, slots, n,
-      err);
-  return cudaGetLastError();
+  return launch_pdl(kv_write_kernel, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, st, c,
+                    (const uint8_t*)k, (const uint8_t*)v, k_stride * c.esize, v_stride * c.esize,
+                    slots, n, err);
 }
 
 }  // namespace dlm

@@ -195,8 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch(&tmQ);
   }
   if (warp == kMma) tmem_alloc(&sh.tmem, kTmemCols);
-  // the join may be set up while this grid runs (it waits for the grid's end)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // the kernel before this one is waited for here; the join may be set up while
+  // this grid runs (it waits for the grid's end)
+  pdl_wait_then_release();
 
   // ---- this CTA's range of the work (the scan's scratch is the ring, free until
   // the first load) ----
@@ -836,8 +837,9 @@ cudaError_t launch(const PagedAttn& a, int num_sms, cudaStream_t st) {
   if (!encode(&tmK, a.c.k, 5, kd, ks, kb) || !encode(&tmV, a.c.v, 5, kd, ks, kb) ||
       !encode(&tmQ, const_cast<void*>(a.q), 3, qd, qst, qb))
     return cudaErrorInvalidValue;
-  paged_attn_kernel<DH><<<num_sms, kThreads, Smem<DH>::kBytes, st>>>(tmK, tmV, tmQ, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_pdl(paged_attn_kernel<DH>, dim3(num_sms), dim3(kThreads), Smem<DH>::kBytes, st, tmK, tmV,
+                 tmQ, p);
+  if (e != cudaSuccess) return e;
   return launch_join<__nv_bfloat16, DH>(p, num_sms, kSlotRows, st);
 }
 

@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_f32_kernel(co
   __shared__ Item item;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ty = tid >> 4, tx = tid & 15;   // rows 4 ty .., keys tx + 16 j, columns DN tx ..
+  pdl_wait_then_release();
   find_range<kThreads>(p, BN, BN, 1, scan, start, stop);
   __syncthreads();
   Walker walk(start, stop);
@@ -282,8 +283,8 @@ cudaError_t launch(const PagedAttn& a, int num_sms, cudaStream_t st) {
   Params p = make_params(a, ctas);
   p.npos = p.G < kRows ? kRows / p.G : 1;
   p.positions = p.npos;
-  paged_attn_f32_kernel<DH><<<ctas, kThreads, Shape<DH>::kBytes, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_pdl(paged_attn_f32_kernel<DH>, dim3(ctas), dim3(kThreads), Shape<DH>::kBytes, st, p);
+  if (e != cudaSuccess) return e;
   return launch_join<float, DH>(p, ctas, p.npos * p.G, st);
 }
 

@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_c
   using Vec = typename std::conditional<
       E == 4, float4, typename std::conditional<E == 2, float2, float>::type>::type;
   constexpr int kTileRows = kSlotRows / 2;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait_then_release();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Meta me = p.meta[c];
   // rows r0 + 8 u of row tile `tile`; those in use are the tile's first ones
