@@ -34,8 +34,15 @@ constexpr int kRows = 128;       // rows per row tile
 constexpr int kThreads = 512;
 constexpr int kProducer = 8, kMma = 9, kScheduler = 11, kWriter = 12;
 constexpr int kDescs = 4;
-constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P over S), O0, O1 (Dh each)
+// Tensor memory: S0, S1 (128 columns each), O0, O1 (Dh each), and P (64 columns of
+// bf16 pairs): for Dh 64 in columns of its own, for Dh 128 in the upper half of its
+// S, whose lower half is then free for the next S
+constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
+template <int DH>
+__device__ __forceinline__ uint32_t col_p(int i) {
+  return DH == 64 ? kColO + 128 + i * 64 : i * kKeys + 64;
+}
 // cost of an item beside its keys, in keys: loading Q, the first S, the epilogue
 constexpr int kItemCost = 128;
 // key tiles of a piece when there is little work (one: the join costs more than
@@ -64,7 +71,7 @@ struct Smem {
     Item item[kDescs];
     float2 stat[2][kRows];   // (max, sum) of the rows, per row tile or half
     uint64_t full[Tile<DH>::kSlots], empty[Tile<DH>::kSlots];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2], turn[2][4];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2], turn[2][4], pv_done[2];
     uint64_t d_full[kDescs], d_empty[kDescs];
     uint64_t stat_full[2], stat_empty[2], fix_req[2], fix_done[2], fin[2];
     int start[4], stop[4];
@@ -176,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.p_full[i][0], 4);   // the first 64 keys' P, the others'
       mbar_init(&sh.p_full[i][1], 4);
       mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.o_empty[i], 4);
       mbar_init(&sh.stat_full[i], 4);
       mbar_init(&sh.stat_empty[i], 4);
@@ -301,9 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // without a move per instruction.
       const int i = warp - kMma;
       constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
+      constexpr uint32_t idesc_h = idesc_bf16_f32(kRows, kKeys / 2);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DH, true);
       const uint32_t tm_s = __shfl_sync(0xffffffffu, tmem + i * kKeys, 0);
-      const uint32_t tm_o = __shfl_sync(0xffffffffu, tmem + kColO + i * 128, 0);
+      const uint32_t tm_o = __shfl_sync(0xffffffffu, tmem + kColO + i * DH, 0);
+      const uint32_t tm_p = __shfl_sync(0xffffffffu, tmem + col_p<DH>(i), 0);
       const uint64_t kd0 = desc_k(smem_u32(ring), TL::kGroup);
       const uint64_t vd0 = desc_mn(smem_u32(ring), TL::kGroup);
       const uint64_t qd0 = desc_k(smem_u32(qs), 1024);
@@ -344,13 +354,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh.q_empty[qi]);
           if (pair) mbar_arrive(&sh.q_empty[qi]);
         }
-        // S_i(l) = Q_i K(l)^T, over the P that the P V before it has read
-        auto issue_s = [&](uint32_t ks) {
-          const uint64_t kd = kd0 + (uint64_t)(ks * (TL::kBytes >> 4));
+        // S_i = Q_i K^T: all 128 keys, or the lower (part 0) or upper (part 1) 64
+        auto issue_s = [&](uint32_t ks, int part) {
+          const bool half = part >= 0;
+          const uint64_t kd = kd0 + (uint64_t)((ks * TL::kBytes + (part == 1 ? 8 * TL::kGroup : 0)) >> 4);
+          const uint32_t d = tm_s + (part == 1 ? 64 : 0), idesc = half ? idesc_h : idesc_s;
 #pragma unroll
           for (int x = 0; x < DH / 16; ++x)
-            umma_bf16(tm_s, qd + (uint64_t)(((x >> 2) * TL::kQHalf + (x & 3) * 32) >> 4),
-                      kd + (uint64_t)(((x >> 2) * 1024 + (x & 3) * 32) >> 4), idesc_s, x > 0);
+            umma_bf16(d, qd + (uint64_t)(((x >> 2) * TL::kQHalf + (x & 3) * 32) >> 4),
+                      kd + (uint64_t)(((x >> 2) * 1024 + (x & 3) * 32) >> 4), idesc, x > 0);
         };
         auto release_q = [&]() {
           umma_commit(&sh.q_empty[qi]);
@@ -367,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (mine && !k_there) {
             tc_fence_after();
             if (elect_one()) {
-              issue_s(slot);
+              issue_s(slot, -1);
               umma_commit(&sh.s_full[i]);
               umma_commit(&sh.empty[slot]);
               if (last) release_q();
@@ -394,11 +406,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = ok && wait(&sh.o_empty[i], no, abort_flag);
               no ^= 1;
             }
-            // two row tiles: the next K first, so that its S follows P V at once
+            // two row tiles: the next K first, so that no wait parts its S from P V
             k_there = pair && !last;
             const uint32_t ks = slot + 1 == NS ? 0 : slot + 1;
             if (k_there) ok = ok && wait(&sh.full[ks], phase ^ (ks == 0 ? 1u : 0u), abort_flag);
-            // in two halves: the first runs during the second's exponentials
+            // P V in two halves, the first during the second's exponentials; with the
+            // first, what of the next S has room (Dh 64: all of it; Dh 128: its lower
+            // half, the upper one after P has been read)
             const uint64_t vd = vd0 + (uint64_t)(slot * (TL::kBytes >> 4));
 #pragma unroll 1
             for (int h = 0; h < 2 && ok; ++h) {
@@ -406,18 +420,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
               tc_fence_after();
               if (elect_one()) {
+                if (DH == 64 && h == 0 && k_there) {
+                  issue_s(ks, -1);
+                  umma_commit(&sh.s_full[i]);
+                  umma_commit(&sh.empty[ks]);
+                }
 #pragma unroll
                 for (int x = 0; x < kKeys / 32; ++x)
-                  umma_bf16_tmem_a(tm_o, tm_s + h * 32 + x * 8,
+                  umma_bf16_tmem_a(tm_o, tm_p + h * 32 + x * 8,
                                    vd + (uint64_t)((h * 8 + x * 2) * TL::kGroup >> 4), idesc_o,
                                    l != first || h > 0 || x > 0);
-                if (h == 1) {
-                  if (k_there) {
-                    issue_s(ks);
+                if (DH == 64 && h == 1) umma_commit(&sh.pv_done[i]);
+                if (DH == 128 && k_there) {
+                  issue_s(ks, h);
+                  if (h == 1) {
                     umma_commit(&sh.s_full[i]);
                     umma_commit(&sh.empty[ks]);
-                    if (l + 1 + step >= limit) release_q();
                   }
+                }
+                if (h == 1) {
+                  if (k_there && l + 1 + step >= limit) release_q();
                   umma_commit(&sh.empty[slot]);
                   if (last) umma_commit(&sh.o_full[i]);
                 }
@@ -571,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               float o[16];
               {
                 uint32_t r0[16], r1[16];
-                tmem_ld16_nowait(o_col + i * 128 + y * 16, r0);
-                if (two) tmem_ld16_nowait(o_col + 128 + y * 16, r1);
+                tmem_ld16_nowait(o_col + i * DH + y * 16, r0);
+                if (two) tmem_ld16_nowait(o_col + DH + y * 16, r1);
                 tmem_wait_ld();
                 // c == 0: no key was seen, and O holds an earlier item's
 #pragma unroll
@@ -629,7 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t s_col = lane_addr + i * kKeys;
-    const uint32_t o_col = lane_addr + kColO + i * 128;
+    const uint32_t o_col = lane_addr + kColO + i * DH;
+    const uint32_t p_col = lane_addr + col_p<DH>(i);
     const int rp = div_g(p, row);                     // position of the row
     uint32_t ns = 0;                                  // S tiles taken
     uint32_t nt = 0;                                  // phase of the next turn
@@ -651,8 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any = __any_sync(0xffffffffu, live);
       // The two row tiles (halves) take turns at the exponentials, each warp with
       // the one that shares its scheduler.  Left alone they fall into step, both
-      // at the exponential unit and then both at the tensor core (prompts case:
-      // 1437 us against 1291 in turns).
+      // at the exponential unit and then both at the tensor core (chunks of up to
+      // 4096 tokens, 32 / 8 heads x 128: 1375 us against 1298 in turns).
       const int turns = min(c0, c1);
       auto take_turn = [&](int x) {
         if (x >= turns) return true;
@@ -665,6 +688,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int x = 0; x < c; ++x, ++ns) {
+        // P V tiles finished when this tile's P is written: all but this item's first
+        // tile's predecessor, which the item before it has waited for
+        const uint32_t npv = ns - 1;
         const int t = it.ts + (pair ? x : 2 * x + i);
         if (!wait(&sh.s_full[i], ns & 1, abort_flag)) {
           ok = false;
@@ -710,7 +736,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m_new = move ? fmaxf(m_run, mx) : m_run;
           const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // no key seen yet
           const float alpha = move ? fast_exp2(m_run - base) : 1.f;
-          // S(x) was issued after P(x-1) V, so O holds every earlier tile
+          // Dh 128: S(x) was finished after P(x-1) V, so O holds every earlier tile and
+          // P's columns are free; Dh 64: wait for that
+          if (DH == 64 && x > 0 && !wait(&sh.pv_done[i], npv & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (DH == 64 && x > 0) tc_fence_after();
           if (x > 0 && move) {
 #pragma unroll 1
             for (int y = 0; y < DH / 32; ++y) {
@@ -723,10 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(-base, -base);
           uint64_t rs[2] = {0, 0};
-          // P in the MMA's operand type, two keys a column, over columns of S that
-          // have been read; the sum keeps float32
-          auto exp32 = [&](const uint32_t (&raw)[32], int y) {
-            uint32_t w[16];
+          // P in the MMA's operand type, two keys a column; the sum keeps float32
+          auto exp32 = [&](const uint32_t (&raw)[32], uint32_t (&w)[16]) {
 #pragma unroll
             for (int z = 0; z < 16; ++z) {
               float e0, e1;
@@ -738,29 +768,36 @@ __global__ void __launch_bounds__(kThreads, 1)
               rs[z & 1] = add2(rs[z & 1], pack2(e0, e1));
               w[z] = pack_bf16(e0, e1);
             }
-            tmem_st16_u(s_col + y * 16, w);
           };
           uint32_t ra[32], rb[32];
           tmem_ld32_nowait(s_col, ra);
+          tmem_ld32_nowait(s_col + 32, rb);
           if (!take_turn(x)) {
             ok = false;
             break;
           }
+          // 64 keys at a time.  The first half's P is announced when all of S has
+          // been read as well: its P V, and what of the next S does not need the
+          // second half, run during the second half's exponentials
 #pragma unroll 1
-          for (int y = 0; y < kKeys / 32; y += 2) {
+          for (int h = 0; h < 2; ++h) {
+            uint32_t wa[16], wb[16];
             tmem_wait_ld();
-            tmem_ld32_nowait(s_col + y * 32 + 32, rb);
-            exp32(ra, y);
-            tmem_wait_ld();
-            if (y + 2 < kKeys / 32) tmem_ld32_nowait(s_col + y * 32 + 64, ra);
-            exp32(rb, y + 1);
-            // P V of these 64 keys may start
+            exp32(ra, wa);
+            if (h == 0) tmem_ld32_nowait(s_col + 64, ra);
+            exp32(rb, wb);
+            if (h == 0) {
+              tmem_ld32_nowait(s_col + 96, rb);
+              tmem_wait_ld();
+            }
+            if (h == 1) pass_turn(x);
+            tmem_st16_u(p_col + h * 32, wa);
+            tmem_st16_u(p_col + h * 32 + 16, wb);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[i][y >> 1]);
+            if (lane == 0) mbar_arrive(&sh.p_full[i][h]);
           }
-          pass_turn(x);
           {
             float s0, s1;
             unpack2(add2(rs[0], rs[1]), s0, s1);
