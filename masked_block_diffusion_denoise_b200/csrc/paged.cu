@@ -240,11 +240,12 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
 // ---------------------------------------------------------------------------
 // K/V rows into their slots: a copy in 16-byte pieces.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) kv_write_kernel(const PagedKV c, const uint8_t* __restrict__ k,
-                                                       const uint8_t* __restrict__ v,
-                                                       int64_t k_stride, int64_t v_stride,
-                                                       const int64_t* __restrict__ slots, int n,
-                                                       int* err) {
+// (No __restrict__: the kernel before, which may write these, can still run
+// when this one starts, so they are not read-only for its whole life.)
+__global__ void __launch_bounds__(256) kv_write_kernel(const PagedKV c, const uint8_t* k,
+                                                       const uint8_t* v, int64_t k_stride,
+                                                       int64_t v_stride, const int64_t* slots,
+                                                       int n, int* err) {
   pdl_wait_then_release();
   const int head_chunks = c.Dh * c.esize / 16;
   const int row_chunks = c.Hkv * head_chunks;

@@ -94,11 +94,10 @@ PagedKV kv_of(const dlm_paged_cache* c) {
 }
 
 // rows of `width` elements, `stride` apart: 16-byte pieces, no overlap
-const char* rows_problem(const void* p, int64_t stride, int64_t width, int esize, int64_t rows) {
+const char* rows_problem(const void* p, int64_t stride, int64_t width, int esize) {
   if (!aligned(p, 16)) return "paged: rows are not 16-byte aligned";
   if (stride < width || stride * esize % 16 != 0 || stride > (1ll << 40))
     return "paged: a row stride must be a multiple of 16 bytes and at least the row";
-  (void)rows;
   return nullptr;
 }
 
@@ -146,9 +145,9 @@ int dlm_paged_kv_write(const dlm_paged_cache* cache, const void* k, const void* 
   if (!k || !v || !slots) return api_fail(DLM_EINVAL, "paged_kv_write: NULL pointer argument");
   const PagedKV c = kv_of(cache);
   const int64_t row = (int64_t)c.Hkv * c.Dh;
-  if (const char* why = rows_problem(k, k_stride, row, c.esize, n_tokens))
+  if (const char* why = rows_problem(k, k_stride, row, c.esize))
     return api_fail(DLM_EINVAL, why);
-  if (const char* why = rows_problem(v, v_stride, row, c.esize, n_tokens))
+  if (const char* why = rows_problem(v, v_stride, row, c.esize))
     return api_fail(DLM_EINVAL, why);
   PagedDevice* d = nullptr;
   int dev = 0;
@@ -193,9 +192,9 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
     return api_fail(DLM_EINVAL, "paged_attention: the workspace is not 256-byte aligned");
   const PagedKV c = kv_of(cache);
   const int64_t row = (int64_t)n_heads * c.Dh;
-  if (const char* why = rows_problem(q, q_stride, row, c.esize, n_tokens))
+  if (const char* why = rows_problem(q, q_stride, row, c.esize))
     return api_fail(DLM_EINVAL, why);
-  if (const char* why = rows_problem(o, o_stride, row, c.esize, n_tokens))
+  if (const char* why = rows_problem(o, o_stride, row, c.esize))
     return api_fail(DLM_EINVAL, why);
   if ((long long)n_tokens * n_heads > INT_MAX)
     return api_fail(DLM_EINVAL, "paged_attention: n_tokens * n_heads exceeds 2^31 - 1");

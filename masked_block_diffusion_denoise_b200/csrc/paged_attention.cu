@@ -162,7 +162,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the tiles' swizzle wants 1024-byte alignment, and there is no room to round up
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {
-    if (threadIdx.x == 0) raise_error(p.err, DLM_EBOUNDS);
+    pdl_wait_then_release();
+    if (threadIdx.x == 0) {
+      raise_error(p.err, DLM_EBOUNDS);
+      p.meta[blockIdx.x] = Meta{};   // nothing to join
+    }
     return;
   }
   uint8_t* qs = smem + Smem<DH>::kQ;
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int chunk = -1, id = 0, id_next = 0;
         auto load_ids = [&](int c) {
           const int i = c * 32 + lane;
-          return i < n_pages ? __ldg(row + i) : 0;
+          return i < n_pages ? row[i] : 0;
         };
         for (int t = ts; t < te && ok; ++t) {
           // page ids, 32 at a time, the next 32 on their way

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_f32_kernel(co
           bool live = k < it.ctx;
           int64_t at = 0;
           if (live) {
-            const int page = __ldg(p.table + (size_t)it.b * p.W + (k >> p.page_shift));
+            const int page = p.table[(size_t)it.b * p.W + (k >> p.page_shift)];
             live = page >= 0 && page < p.n_pages;
             if (live)
               at = ((((int64_t)page * p.Hkv + it.g) << p.page_shift) + (k & page_mask)) * DH + c;

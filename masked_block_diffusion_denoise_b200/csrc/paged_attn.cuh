@@ -132,8 +132,12 @@ __device__ __forceinline__ int div_g(const Params& p, int x) {
   return (int)(((uint32_t)x * p.g_inv) >> 16);
 }
 
+// Offsets ascending within the rows, a length that the table can hold (and that
+// leaves room for a tile's end in 32 bits).  cu, ctx and table are read with
+// plain loads: the kernel before, which may write them, can still run when this
+// one starts, so they are not read-only for its whole life.
 __device__ __forceinline__ bool seq_ok(const Params& p, int c0, int c1, int ctx) {
-  return c0 >= 0 && c0 <= c1 && c1 <= p.T && ctx >= 0 &&
+  return c0 >= 0 && c0 <= c1 && c1 <= p.T && ctx >= 0 && ctx <= 0x7FFF0000 &&
          (long long)ctx <= ((long long)p.W << p.page_shift);
 }
 
@@ -186,8 +190,8 @@ __device__ void find_range(const Params& p, int key_tile, int item_cost, int min
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   // the sequence's new tokens and length; none if the input is bad
   auto sequence = [&](int b, int& n, int& ctx, bool report) {
-    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
-    ctx = __ldg(p.ctx + b);
+    const int c0 = p.cu[b], c1 = p.cu[b + 1];
+    ctx = p.ctx[b];
     n = c1 - c0;
     if (!seq_ok(p, c0, c1, ctx)) {
       if (report) raise_error(p.err, DLM_EBOUNDS);
@@ -310,9 +314,9 @@ struct Walker {
         cb = b >> 5;
         const int bb = cb * 32 + lane;
         const bool in = bb < p.B;
-        l0 = in ? __ldg(p.cu + bb) : 0;
-        l1 = in ? __ldg(p.cu + bb + 1) : 0;
-        lc = in ? __ldg(p.ctx + bb) : 0;
+        l0 = in ? p.cu[bb] : 0;
+        l1 = in ? p.cu[bb + 1] : 0;
+        lc = in ? p.ctx[bb] : 0;
         if (!in || !seq_ok(p, l0, l1, lc)) l1 = l0 = 0;
       }
       const int c0 = __shfl_sync(0xffffffffu, l0, b & 31);

@@ -473,6 +473,63 @@ def test_attention_reports_bad_inputs():
                 assert (np.abs(f64(o[10:]) - ref) <= 2.0 ** -7 * (a + np.abs(ref))).all(), kind
 
 
+def reference(p, q, new, heads, block):
+    """attend() of every sequence in float64 on the GPU (larger sizes)."""
+    o, a, row = torch.zeros(q.shape, dtype=torch.float64, device="cuda"), None, 0
+    a, lse = torch.zeros_like(o), torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device="cuda")
+    g = heads // p.kv
+    for b, n in enumerate(new):
+        ctx = p.ctx[b]
+        pos = torch.arange(ctx - n, ctx, device="cuda")
+        lim = torch.full_like(pos, ctx) if block == 0 else \
+            torch.where(pos < 0, 0, ((pos // block + 1) * block).clamp(max=ctx))
+        for h in range(heads if n and ctx else 0):
+            k, v = p.k[b][:, h // g].double(), p.v[b][:, h // g].double()
+            s = q[row:row + n, h].double() @ k.T / math.sqrt(p.dim)
+            s = torch.where(torch.arange(ctx, device="cuda") < lim[:, None], s, -math.inf)
+            seen = lim > 0
+            e = torch.softmax(s[seen], 1)
+            o[row:row + n, h][seen] = e @ v
+            a[row:row + n, h][seen] = e @ v.abs()
+            lse[row:row + n, h][seen] = torch.logsumexp(s[seen], 1)
+        row += n
+    return o, a, lse
+
+
+@pytest.mark.parametrize("dtype,heads,kv,dim,page,seqs,block", [
+    ("bf16", 8, 2, 128, 16, [(20000, 33), (70, 70), (9000, 1)], 0),       # one long sequence
+    ("bf16", 8, 2, 128, 64, [(5000, 1500), (640, 640), (3, 3)], 1),       # more work than SMs
+    ("bf16", 16, 4, 64, 32, [(2600, 1333), (257, 200)], 256),
+    ("bf16", 3, 3, 128, 128, [(1700, 900)], 1),                           # G 1
+    ("f32", 4, 2, 64, 32, [(6000, 70), (300, 300)], 1),
+    ("f32", 6, 1, 128, 16, [(1500, 257)], 0),
+])
+def test_attention_larger(dtype, heads, kv, dim, page, seqs, block):
+    p = Paged(dtype, kv, dim, page, [c for c, _ in seqs], seed=31)
+    new = [n for _, n in seqs]
+    q = ready(p, new, heads, 31)
+    o, lse, _ = p.attend(q, new, heads, block)
+    ref, a, rl = reference(p, q, new, heads, block)
+    # roundings of p and of the result by u, and a part in 2^12 (bf16) or 2^18 (f32) of
+    # sum p |v| for scores up to about 8 and sums of up to 20000 terms in float32
+    u, rest = (2.0 ** -8, 2.0 ** -12) if dtype == "bf16" else (2.0 ** -24, 2.0 ** -18)
+    tol = a * ((u if dtype == "bf16" else 0) * 1.01 + rest) + u * ref.abs()
+    assert bool(((o.double() - ref).abs() <= tol).all())
+    assert float((lse.double() - rl).abs().max()) <= rest
+
+
+@pytest.mark.parametrize("batch,dtype", [(700, "bf16"), (4096, "bf16"), (700, "f32")])
+def test_attention_many_sequences(batch, dtype):
+    """More sequences than threads, a third of them empty, chunks of 0..3 tokens."""
+    rng = np.random.default_rng(batch)
+    ctx = [int(x) for x in rng.integers(0, 40, batch)]
+    new = [min(c, int(x)) if rng.random() < 0.7 else 0 for c, x in zip(ctx, rng.integers(0, 4, batch))]
+    p = Paged(dtype, 2, 64, 8, ctx, seed=batch)
+    q = ready(p, new, 4, batch)
+    o, lse, cu = p.attend(q, new, 4, 1)
+    check(p, q, o, lse, cu, new, 4, 1)
+
+
 def test_attention_deterministic():
     p = Paged("bf16", 2, 128, 16, [3000, 5, 700], seed=6)
     new = [30, 5, 200]
@@ -610,6 +667,72 @@ def test_captured_step_follows_device_lengths():
         assert torch.all(o[at:] == 5)
         host = target
     assert lens.tolist() == host
+
+
+def test_first_calls_inside_a_capture():
+    """The first use of every call in a process may be the captured one."""
+    script = """
+import torch
+import masked_block_diffusion_denoise_b200 as dlm
+z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device="cuda")
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+kc, vc = z(8, 2, 16, 128), z(8, 2, 16, 128)
+c = dlm.dlm_paged_cache(kc.data_ptr(), vc.data_ptr(), 8, 16, 2, 128, dlm.DLM_BF16)
+work = z(dlm.dlm_paged_attention_workspace(c, 8), t=torch.uint8)
+lens, want, table, free, nf = i([0]), i([20]), z(1, 4, t=torch.int32), torch.arange(8, dtype=torch.int32, device="cuda"), i([8])
+cu, slots = z(2, t=torch.int32), z(24, t=torch.int64)
+q, k, v, o = z(24, 8, 128) + 1, z(24, 2, 128) + 1, z(24, 2, 128) + 2, z(24, 8, 128)
+torch.cuda.synchronize()
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(g, stream=s):
+    dlm.dlm_paged_resize(lens, want, lens, 1, table, 4, 16, free, 8, nf, nf, cu, slots, 24, stream=s)
+    dlm.dlm_paged_kv_write(c, k, v, slots, 24, stream=s)
+    dlm.dlm_paged_attention(c, q, o, cu, lens, table, 4, 1, 24, 8, 1, work, stream=s)
+g.replay()
+torch.cuda.synchronize()
+dlm.dlm_paged_check()
+assert torch.all(o[:20] == 2) and torch.all(o[20:] == 0), o
+print("fine")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_back_to_back_calls_see_each_other():
+    """Resize, write and attend in a row without a pause, many times: the kernels'
+    overlapping starts must not read what the one before has yet to write."""
+    kv, heads, dim, page, B = 2, 8, 128, 16, 64
+    n_pages, width = 1024, 16
+    kc = torch.zeros((n_pages, kv, page, dim), dtype=torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    cache = dlm.dlm_paged_cache(kc.data_ptr(), vc.data_ptr(), n_pages, page, kv, dim, dlm.DLM_BF16)
+    work = torch.empty(dlm.dlm_paged_attention_workspace(cache, heads), dtype=torch.uint8, device="cuda")
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(n_pages, dtype=torch.int32, device="cuda")
+    nf, lens, cu = i32([n_pages]), i32([0] * B), torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    wants = [i32([0] * B), i32([33] * B), i32([b % 40 for b in range(B)])]
+    slots = torch.empty(B * 40, dtype=torch.int64, device="cuda")
+    q = torch.ones((B * 40, heads, dim), dtype=torch.bfloat16, device="cuda")
+    k = torch.ones((B * 40, kv, dim), dtype=torch.bfloat16, device="cuda")
+    outs = []
+    for r in range(60):
+        v = torch.full((B * 40, kv, dim), float(r % 7 + 1), dtype=torch.bfloat16, device="cuda")
+        o = torch.zeros((B * 40, heads, dim), dtype=torch.bfloat16, device="cuda")
+        for w in (wants[0], wants[1 + r % 2]):
+            dlm.dlm_paged_resize(lens, w, lens, B, table, width, page, free, n_pages, nf, nf, cu, slots,
+                                 B * 40)
+            dlm.dlm_paged_kv_write(cache, k, v, slots, B * 40)
+            dlm.dlm_paged_attention(cache, q, o, cu, lens, table, width, B, B * 40, heads, 1, work)
+        outs.append((r, o))
+    dlm.dlm_paged_check()
+    for r, o in outs:
+        total = int(wants[1 + r % 2].sum())
+        assert torch.all(o[:total] == r % 7 + 1) and torch.all(o[total:] == 0), r
 
 
 def test_host_pointers_are_refused():
