@@ -173,17 +173,13 @@ def lib() -> ctypes.CDLL:
 
 def _ptr(x) -> Optional[int]:
     """Device/host address of a torch tensor, an int, or None."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
     return x.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        return None
-    if isinstance(stream, int):
+    if stream is None or stream.__class__ is int:
         return stream
     return stream.cuda_stream
 

@@ -280,6 +280,7 @@ cudaError_t paged_resize(const PagedResize& a, cudaStream_t st) {
   // one CTA up to a run of slots a thread, then a cluster of up to 8
   int ranks = 1;
   while (ranks < 8 && (long long)ranks * kRun * kResizeThreads < a.max_new) ranks *= 2;
+  if (ranks == 1) return launch_pdl(resize_kernel, dim3(1), dim3(kResizeThreads), smem, st, a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);
   cfg.blockDim = dim3(kResizeThreads);

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's range of the work (the scan's scratch is the ring, free until
   // the first load) ----
-  find_range<kThreads>(p, kKeys, kItemCost, kMinTiles, reinterpret_cast<long long*>(ring), sh.start,
+  find_range<kThreads>(p, kKeys, kItemCost, kMinTiles, reinterpret_cast<longlong2*>(ring), sh.start,
                        sh.stop);
   fence_proxy_async_smem();
   tc_fence_before();

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_f32_kernel(co
   float* vs = sm + SH::kV;   // [2][BN][DH]
   float* ps = sm + SH::kP;   // [kRows][kLdP]
   __shared__ int start[4], stop[4];
-  __shared__ long long scan[2 * kThreads / 32];
+  __shared__ longlong2 scan[kThreads / 32];
   __shared__ Item item;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ty = tid >> 4, tx = tid & 15;   // rows 4 ty .., keys tx + 16 j, columns DN tx ..

@@ -141,27 +141,38 @@ __device__ __forceinline__ bool seq_ok(const Params& p, int c0, int c1, int ctx)
          (long long)ctx <= ((long long)p.W << p.page_shift);
 }
 
-// The block's exclusive scan of x; *total its sum.  `scan`: shared memory, a
-// number per warp.
+// The block's exclusive scans of x and y; the sums in *all.  `scan`: shared
+// memory, a pair per warp.
 template <int THREADS>
-__device__ __forceinline__ long long block_scan(long long x, long long* scan, long long* total) {
+__device__ __forceinline__ longlong2 block_scan(longlong2 x, longlong2* scan, longlong2* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl = x;
+  longlong2 incl = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
+    const long long a = __shfl_up_sync(0xffffffffu, incl.x, d);
+    const long long b = __shfl_up_sync(0xffffffffu, incl.y, d);
+    if (lane >= d) {
+      incl.x += a;
+      incl.y += b;
+    }
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  long long before = 0, all = 0;
+  longlong2 before = make_longlong2(0, 0);
+  *all = make_longlong2(0, 0);
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    if (w == warp) before = all;
-    all += scan[w];
+    if (w == warp) before = *all;
+    all->x += scan[w].x;
+    all->y += scan[w].y;
   }
-  *total = all;
-  return before + incl - x;
+  return make_longlong2(before.x + incl.x - x.x, before.y + incl.y - x.y);
+}
+
+// the page ids of a sequence from key k on are needed soon
+__device__ __forceinline__ void prefetch_pages(const Params& p, int b, int k) {
+  const int col = min(k >> p.page_shift, p.W - 1);
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p.table + (size_t)b * p.W + col));
 }
 
 // u / w, by a double's quotient and a correction (u < 2^53)
@@ -179,11 +190,11 @@ __device__ __forceinline__ int small_quotient(long long u, long long w) {
 //   pieces than CTAs): a piece per CTA, so that none has two items.
 //   Else all items, KV head by KV head, are laid end to end in units of cost
 //   and cut into equal shares.
-// `scan`: shared memory, two numbers per warp.  The caller synchronises before
+// `scan`: shared memory, a pair of numbers per warp.  The caller synchronises before
 // it reads start and stop.
 template <int THREADS>
 __device__ void find_range(const Params& p, int key_tile, int item_cost, int min_tiles,
-                           long long* scan, int* start, int* stop) {
+                           longlong2* scan, int* start, int* stop) {
   const int tid = threadIdx.x;
   const int pp = p.positions;
   const int per = (p.B + THREADS - 1) / THREADS;
@@ -203,41 +214,44 @@ __device__ void find_range(const Params& p, int key_tile, int item_cost, int min
     const int i1 = min(n, (j + 1) * pp);
     return (visible(ctx - n + i1 - 1, ctx, p.block) + key_tile - 1) / key_tile;
   };
+  // pieces of min_tiles key tiles
+  auto pieces = [&](int n, int ctx, int j) {
+    return max(1, (tiles(n, ctx, j) + min_tiles - 1) / min_tiles);
+  };
   if (tid < 4) start[tid] = stop[tid] = 0;
-  long long mine = 0, w1;
+  // a sequence's cost, and its pieces unless its keys alone make more than the grid
+  const long long few = (long long)gridDim.x * min_tiles * key_tile;
+  longlong2 own = make_longlong2(0, 0), sum;
   for (int b = b0; b < b1; ++b) {
     int n, ctx;
     sequence(b, n, ctx, blockIdx.x == 0);
     const SeqCost s(n, ctx, pp, p.block, item_cost);
-    mine += s.cum(s.items);
+    const long long c = s.cum(s.items);
+    own.x += c;
+    if ((c - (long long)s.items * item_cost) * p.Hkv > few || own.y > gridDim.x)
+      own.y = gridDim.x + 1;
+    else
+      for (int j = 0; j * pp < n; ++j) own.y += pieces(n, ctx, j);
   }
-  long long first = block_scan<THREADS>(mine, scan, &w1);
-  const long long total = w1 * p.Hkv;
-  if (total <= (long long)gridDim.x * (min_tiles * key_tile + item_cost)) {
-    auto pieces = [&](int n, int ctx, int j) {
-      return max(1, (tiles(n, ctx, j) + min_tiles - 1) / min_tiles);
-    };
-    long long own = 0, all;
-    for (int b = b0; b < b1; ++b) {
-      int n, ctx;
-      sequence(b, n, ctx, false);
-      for (int j = 0; j * pp < n; ++j) own += pieces(n, ctx, j);
-    }
-    const long long before = block_scan<THREADS>(own, scan + THREADS / 32, &all);
+  const longlong2 before = block_scan<THREADS>(own, scan, &sum);
+  const long long mine = own.x, first = before.x, w1 = sum.x, total = w1 * p.Hkv;
+  {
+    const long long all = sum.y;
     if (all * p.Hkv <= gridDim.x) {
       if ((int)blockIdx.x >= all * p.Hkv) {
         if (tid == 0) start[0] = stop[0] = p.Hkv;
         return;
       }
       const int g = (int)blockIdx.x / (int)all;
-      int r = (int)blockIdx.x - g * (int)all - (int)before;
-      if (r < 0 || r >= own) return;
+      int r = (int)blockIdx.x - g * (int)all - (int)before.y;
+      if (r < 0 || r >= own.y) return;
       for (int b = b0; b < b1; ++b) {
         int n, ctx;
         sequence(b, n, ctx, false);
         for (int j = 0; j * pp < n; ++j) {
           const int k = pieces(n, ctx, j);
           if (r < k) {
+            prefetch_pages(p, b, r * min_tiles * key_tile);
             start[0] = stop[0] = g;
             start[1] = stop[1] = b;
             start[2] = j;
@@ -286,6 +300,7 @@ __device__ void find_range(const Params& p, int key_tile, int item_cost, int min
       // the range behind this edge
       const float at = (float)(r - s.cum(lo)), cost = (float)(s.cum(lo + 1) - s.cum(lo));
       const int kt = tiles(n, ctx, lo);
+      if (e == 0) prefetch_pages(p, b, (int)__fdividef(at * kt, cost) * key_tile);
       dst[0] = g;
       dst[1] = b;
       dst[2] = lo;
