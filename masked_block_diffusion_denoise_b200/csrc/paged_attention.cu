@@ -352,12 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             (pair && !wait(&sh.q_full[q0 ^ 1], ((qn + 1) >> 1) & 1, abort_flag)))
           break;
         const uint64_t qd = qd0 + (uint64_t)(qi * (TL::kQBytes >> 4));
+        // A Q tile is free again when both issuers have said so, the one that does not
+        // use it as soon as it has seen it come: it would otherwise miss the next one
+        if (pair && lane == 0) mbar_arrive(&sh.q_empty[qi ^ 1]);
         int own = first;   // the next own tile
-        if (own >= limit && lane == 0) {
-          // no tile here (a row tile without keys, a half without a key tile)
-          mbar_arrive(&sh.q_empty[qi]);
-          if (pair) mbar_arrive(&sh.q_empty[qi]);
-        }
+        // no tile here (a row tile without keys, a half without a key tile)
+        if (own >= limit && lane == 0) mbar_arrive(&sh.q_empty[qi]);
         // S_i = Q_i K^T: all 128 keys, or the lower (part 0) or upper (part 1) 64
         auto issue_s = [&](uint32_t ks, int part) {
           const bool half = part >= 0;
@@ -367,10 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < DH / 16; ++x)
             umma_bf16(d, qd + (uint64_t)(((x >> 2) * TL::kQHalf + (x & 3) * 32) >> 4),
                       kd + (uint64_t)(((x >> 2) * 1024 + (x & 3) * 32) >> 4), idesc, x > 0);
-        };
-        auto release_q = [&]() {
-          umma_commit(&sh.q_empty[qi]);
-          if (pair) umma_commit(&sh.q_empty[qi]);   // one for each issuer
         };
         bool k_there = false;   // S(l) is issued already
         for (int l = 0; l < L; ++l) {
@@ -386,13 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               issue_s(slot, -1);
               umma_commit(&sh.s_full[i]);
               umma_commit(&sh.empty[slot]);
-              if (last) release_q();
+              if (last) umma_commit(&sh.q_empty[qi]);
               if (l == 0 && n == 0) DLM_TRACE_MARK(3);
             }
           } else if (!mine && lane == 0) {
             mbar_arrive(&sh.empty[slot]);
           }
           // the V check may look at V(l): both issuers are done with what its slot held
+          // (and with the check before it, so at most one request is open)
           if (l >= fix_l && lane == 0) mbar_arrive(&sh.fix_req[(fb + (l - fix_l)) & 1]);
           __syncwarp();
           advance();
@@ -400,12 +397,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
+          // both issuers wait for the V check, the one that does not use this V as well:
+          // else it could ask for a check two further on, which would count as the
+          // other's request for this one
+          if (l >= fix_l) {
+            const uint32_t k = fb + (l - fix_l);
+            if (!wait(&sh.fix_done[k & 1], (k >> 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+          }
           if (mine) {
             // O_i (+)= P_i(l) V(l)
-            if (l >= fix_l) {
-              const uint32_t k = fb + (l - fix_l);
-              ok = wait(&sh.fix_done[k & 1], (k >> 1) & 1, abort_flag);
-            }
             if (l == first) {
               ok = ok && wait(&sh.o_empty[i], no, abort_flag);
               no ^= 1;
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
                 if (h == 1) {
-                  if (k_there && l + 1 + step >= limit) release_q();
+                  if (k_there && l + 1 + step >= limit) umma_commit(&sh.q_empty[qi]);
                   umma_commit(&sh.empty[slot]);
                   if (last) umma_commit(&sh.o_full[i]);
                 }
@@ -701,6 +704,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (ns == 0 && tid == 0) DLM_TRACE_MARK(4);
+        // Dh 128: S(x) was finished after P(x-1) V, so O holds every earlier tile and P's
+        // columns are free; Dh 64: wait for that (warps without rows as well: they
+        // must not announce a P before the last one has been taken)
+        if (DH == 64 && x > 0 && !wait(&sh.pv_done[i], npv & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         if (any) {   // warps without rows leave their lanes of P as they are
           const int left = lim - t * kKeys;
@@ -740,13 +750,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m_new = move ? fmaxf(m_run, mx) : m_run;
           const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // no key seen yet
           const float alpha = move ? fast_exp2(m_run - base) : 1.f;
-          // Dh 128: S(x) was finished after P(x-1) V, so O holds every earlier tile and
-          // P's columns are free; Dh 64: wait for that
-          if (DH == 64 && x > 0 && !wait(&sh.pv_done[i], npv & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (DH == 64 && x > 0) tc_fence_after();
           if (x > 0 && move) {
 #pragma unroll 1
             for (int y = 0; y < DH / 32; ++y) {

@@ -501,6 +501,17 @@ def reference(p, q, new, heads, block):
     ("bf16", 8, 2, 128, 64, [(5000, 1500), (640, 640), (3, 3)], 1),       # more work than SMs
     ("bf16", 16, 4, 64, 32, [(2600, 1333), (257, 200)], 256),
     ("bf16", 3, 3, 128, 128, [(1700, 900)], 1),                           # G 1
+    # row tiles whose limits lie many key tiles apart (a block boundary between them)
+    ("bf16", 2, 2, 64, 16, [(2100, 1500), (1100, 1100)], 1000),
+    ("bf16", 4, 4, 64, 64, [(600, 600), (700, 650), (300, 300)] * 8, 512),
+    ("bf16", 4, 2, 128, 16, [(900, 900), (1300, 700)] * 6, 400),
+    # many short items of two row tiles and of one, a key tile or a few each
+    ("bf16", 512, 4, 64, 16, [(303, 5), (123, 8), (340, 5), (512, 1), (432, 7), (519, 8), (194, 1),
+                              (310, 2), (35, 0), (491, 7), (248, 0), (413, 4)], 600),
+    ("bf16", 256, 2, 128, 8, [(100, 7), (123, 8), (40, 5), (12, 1), (232, 7)] * 6, 1),
+    # row tiles with a few rows in the last warps (G 33, 5)
+    ("bf16", 66, 2, 64, 32, [(500, 40), (301, 7)], 1),
+    ("bf16", 20, 4, 64, 16, [(700, 30), (1301, 27)] * 3, 0),
     ("f32", 4, 2, 64, 32, [(6000, 70), (300, 300)], 1),
     ("f32", 6, 1, 128, 16, [(1500, 257)], 0),
 ])
