@@ -541,16 +541,16 @@ inline Params make_params(const PagedAttn& a, int ctas) {
   return p;
 }
 
-// `rows`: of an item at most.  With few rows altogether (n_tokens x n_heads up to
+// `rows`: of a slot at most (the second row tile's begin at kSlotRows / 2).  With few rows altogether (n_tokens x n_heads up to
 // 16384) a row per warp, so that more SMs join; else four, so that the chains of
 // loads are fewer (canvas of 32 tokens, 32 heads: 22.4 us against 18.8 for the call;
 // chunks of up to 4096: the other way round, 15 us more).
 template <typename T, int DH>
 cudaError_t launch_join(const Params& p, int ctas, int rows, cudaStream_t st) {
-  rows = min(rows, (int)min((long long)kSlotRows, (long long)p.T * p.G));
+  if (p.T <= p.npos) rows = min(rows, p.T * p.G);   // one row tile at most
   if ((long long)p.T * p.H <= 16384)
     return launch_pdl(paged_join_kernel<T, DH, 1>, dim3(ctas, (rows + 7) / 8), dim3(256), 0, st, p, ctas);
-  return launch_pdl(paged_join_kernel<T, DH, 4>, dim3(ctas, (kSlotRows + 31) / 32), dim3(256), 0, st, p,
+  return launch_pdl(paged_join_kernel<T, DH, 4>, dim3(ctas, (rows + 31) / 32), dim3(256), 0, st, p,
                     ctas);
 }
 

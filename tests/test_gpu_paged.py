@@ -512,6 +512,7 @@ def reference(p, q, new, heads, block):
     # row tiles with a few rows in the last warps (G 33, 5)
     ("bf16", 66, 2, 64, 32, [(500, 40), (301, 7)], 1),
     ("bf16", 20, 4, 64, 16, [(700, 30), (1301, 27)] * 3, 0),
+    ("bf16", 33, 1, 128, 8, [(780, 6)], 0),      # joined rows of a second row tile
     ("f32", 4, 2, 64, 32, [(6000, 70), (300, 300)], 1),
     ("f32", 6, 1, 128, 16, [(1500, 257)], 0),
 ])
