@@ -15,7 +15,9 @@ import torch
 from . import (DLM_BF16, DLM_F32, DLM_MASK, DLM_UNIFORM, dlm_canvas, dlm_canvas_init,
                dlm_canvas_stats, dlm_check, dlm_commit, dlm_create, dlm_debug_buffer,
                dlm_debug_logits, dlm_decode_block, dlm_decode_block_host, dlm_denoise_step, dlm_generate,
-               dlm_destroy, dlm_kv_append, dlm_model_desc, dlm_sampler_params, dlm_weights)
+               dlm_destroy, dlm_kv_append, dlm_model_desc, dlm_paged_attention,
+               dlm_paged_attention_workspace, dlm_paged_cache, dlm_paged_check,
+               dlm_paged_kv_write, dlm_paged_resize, dlm_sampler_params, dlm_weights)
 
 _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
 _NP_TYPESTR = {torch.float32: "<f4", torch.bfloat16: "<u2", torch.int32: "<i4",
@@ -192,3 +194,74 @@ class Session:
         out = torch.empty((batch * C, self.shape.vocab), dtype=torch.float32, device=self.device)
         dlm_debug_logits(self.ctx, batch, C, out)
         return out
+
+
+class PagedCache:
+    """A paged KV cache for a batch of sequences whose lengths differ: pages,
+    block tables, free list and lengths as device tensors, and one step's calls
+    in order -- resize(), write(), attend().  Nothing reads the lengths back, so
+    a step can be captured into a CUDA graph (its tensors are then reused)."""
+
+    def __init__(self, *, n_pages: int, page_size: int, n_heads: int, n_kv_heads: int,
+                 head_dim: int, batch: int, max_len: int, max_new: int, dtype: str = "bf16",
+                 device="cuda:0"):
+        dev = self.device = torch.device(device)
+        self.dtype = _TORCH[dtype]
+        self.page_size, self.n_heads, self.batch, self.max_new = page_size, n_heads, batch, max_new
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        self.k = torch.empty(shape, dtype=self.dtype, device=dev)
+        self.v = torch.empty(shape, dtype=self.dtype, device=dev)
+        self.width = -(-max_len // page_size)
+        self.table = torch.full((batch, self.width), -1, dtype=torch.int32, device=dev)
+        self.free = torch.arange(n_pages, dtype=torch.int32, device=dev)
+        self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=dev)
+        self.lens = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self.cu = torch.zeros(batch + 1, dtype=torch.int32, device=dev)
+        self.slots = torch.full((max_new,), -1, dtype=torch.int64, device=dev)
+        self.c = dlm_paged_cache(self.k.data_ptr(), self.v.data_ptr(), n_pages, page_size,
+                                 n_kv_heads, head_dim, DLM_BF16 if dtype == "bf16" else DLM_F32)
+        with torch.cuda.device(dev):
+            self.work = torch.empty(dlm_paged_attention_workspace(self.c, n_heads),
+                                    dtype=torch.uint8, device=dev)
+
+    def resize(self, new_lens: torch.Tensor, stream=None) -> None:
+        """Lengths (int32 [batch], device) that the sequences are to have; a
+        sequence that does not get its pages keeps its length (see .lens)."""
+        dlm_paged_resize(self.lens, new_lens, self.lens, self.batch, self.table, self.width,
+                         self.page_size, self.free, self.k.shape[0], self.n_free, self.n_free,
+                         self.cu, self.slots, self.max_new, stream=stream)
+
+    def write(self, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+        """K and V of the last resize's new tokens, [<= max_new][n_kv_heads][head_dim]
+        in sequence order (rows may be strided)."""
+        if k.shape[0] != v.shape[0] or k.shape[0] > self.max_new:
+            raise ValueError("write: k and v have one row per new token, at most max_new")
+        self._rows(k, "k")
+        self._rows(v, "v")
+        dlm_paged_kv_write(self.c, k, v, self.slots, k.shape[0], k_stride=k.stride(0),
+                           v_stride=v.stride(0), stream=stream)
+
+    def attend(self, q: torch.Tensor, mask_block: int, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention of the new tokens' queries [rows][n_heads][head_dim] over their
+        sequences; mask_block 0 (every key), 1 (causal) or a block length."""
+        self._rows(q, "q")
+        if out is None:
+            out = torch.empty((q.shape[0], self.n_heads, self.k.shape[3]), dtype=self.dtype,
+                              device=self.device)
+        self._rows(out, "out")
+        if out.shape != q.shape or q.shape[1] != self.n_heads:
+            raise ValueError("attend: q and out are [rows][n_heads][head_dim]")
+        dlm_paged_attention(self.c, q, out, self.cu, self.lens, self.table, self.width, self.batch,
+                            q.shape[0], self.n_heads, mask_block, self.work, lse=lse,
+                            q_stride=q.stride(0), o_stride=out.stride(0), stream=stream)
+        return out
+
+    def check(self, stream=None) -> None:
+        dlm_paged_check(stream)
+
+    def _rows(self, t: torch.Tensor, what: str) -> None:
+        if (t.dtype != self.dtype or t.dim() != 3 or t.shape[2] != self.k.shape[3] or
+                t.stride(2) != 1 or t.stride(1) != t.shape[2]):
+            raise ValueError("%s: [rows][heads][head_dim] of the cache's type, heads without gaps"
+                             % what)

@@ -614,6 +614,46 @@ def test_a_run_of_steps():
     assert sorted(used + free[:int(nf)].tolist()) == list(range(n_pages))
 
 
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f32", 64)])
+def test_paged_cache_object(dtype, dim):
+    """session.PagedCache: two requests, a canvas with a rollback, a clean pass over
+    the finished block, against the contiguous definition."""
+    from masked_block_diffusion_denoise_b200.session import PagedCache
+    heads, kv = 4, 2
+    pc = PagedCache(n_pages=40, page_size=16, n_heads=heads, n_kv_heads=kv, head_dim=dim, batch=2,
+                    max_len=200, max_new=160, dtype=dtype)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    host, hk, hv = [0, 0], [np.zeros((0, kv, dim))] * 2, [np.zeros((0, kv, dim))] * 2
+    for want, block in (([70, 45], 1), ([102, 77], 0), ([70, 45], 0), ([102, 77], 32), ([0, 78], 1)):
+        pc.resize(i32(want))
+        new = [max(0, w - h) for w, h in zip(want, host)]
+        rows = sum(new)
+        x = torch.randn((rows, heads + 2 * kv, dim), generator=g, device="cuda").to(pc.dtype)
+        q, k, v = x[:, :heads], x[:, heads:heads + kv], x[:, heads + kv:]
+        pc.write(k, v)
+        o = pc.attend(q, block)
+        pc.check()
+        at = 0
+        for b in range(2):
+            sl = slice(at, at + new[b])
+            hk[b] = np.concatenate([hk[b][:want[b]], f64(k[sl])])
+            hv[b] = np.concatenate([hv[b][:want[b]], f64(v[sl])])
+            if new[b]:
+                ref, _, a, mag = OP.attend(f64(q[sl]), hk[b], hv[b], want[b], block)
+                # probabilities and results rounded once each; scores' and sums' f32 roundings
+                u, up = (2.0 ** -8, 2.0 ** -8) if dtype == "bf16" else (2.0 ** -24, 0.0)
+                rest = 2 * (mag * (dim + 4) + want[b] + 2) * 2.0 ** -23
+                tol = 1.01 * a * (up + rest[..., None]) + u * np.abs(ref)
+                assert (np.abs(f64(o[sl]) - ref) <= tol).all()
+            at += new[b]
+        host = want
+    assert pc.lens.tolist() == [0, 78] and int(pc.n_free) == 40 - OP.pages(78, 16)
+    with pytest.raises(ValueError):
+        pc.write(k.float().double(), v)
+    with pytest.raises(ValueError):
+        pc.attend(q[:, :2], 1)
+
+
 def test_captured_step_follows_device_lengths():
     """One graph of resize, write and attend, replayed while the lengths on
     the device change, beside an eager call on another stream with its own
