@@ -383,8 +383,8 @@ int dlm_attention_noalloc_check(void *stream);
  *   slot         page * page_size + offset in the page, int64.
  *   free list    a stack: free_pages[0 .. n_free) are the unused page ids.
  *
- * All pointers are device pointers of the current device (DLM_EINVAL
- * otherwise), and `stream` belongs to it.  Errors found on the device (a page id
+ * All pointers are device pointers of the current device, aligned to their
+ * type (DLM_EINVAL otherwise), and `stream` belongs to it.  Errors found on the device (a page id
  * outside the cache, lengths or offsets out of range, a bounded wait that ran
  * out) are recorded in a word of the device that dlm_paged_check reads; the
  * access is skipped. */

@@ -62,6 +62,7 @@ int page_shift(int page_size) {
 }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+const char* const kUnaligned = "paged: an array is not aligned to its element type";
 
 // the checks of a cache that need no device
 const char* cache_problem(const dlm_paged_cache* c) {
@@ -119,6 +120,11 @@ int dlm_paged_resize(const int32_t* cur_lens, const int32_t* new_lens, int32_t* 
     return api_fail(DLM_EINVAL,
                     "paged_resize: need 1 <= batch <= 4096, table_width and n_pages >= 1, "
                     "0 <= max_new <= 2^30 and a page_size of 8, 16, 32, 64, 128 or 256");
+  for (const void* p : {(const void*)cur_lens, (const void*)new_lens, (const void*)out_lens,
+                        (const void*)block_table, (const void*)free_pages, (const void*)n_free_in,
+                        (const void*)n_free_out, (const void*)cu_new})
+    if (!aligned(p, 4)) return api_fail(DLM_EINVAL, kUnaligned);
+  if (!aligned(slots, 8)) return api_fail(DLM_EINVAL, kUnaligned);
   PagedDevice* d = nullptr;
   int dev = 0;
   if (int rc = paged_device(&d, &dev)) return rc;
@@ -143,6 +149,7 @@ int dlm_paged_kv_write(const dlm_paged_cache* cache, const void* k, const void* 
   if (n_tokens < 0) return api_fail(DLM_EINVAL, "paged_kv_write: n_tokens < 0");
   if (n_tokens == 0) return DLM_OK;
   if (!k || !v || !slots) return api_fail(DLM_EINVAL, "paged_kv_write: NULL pointer argument");
+  if (!aligned(slots, 8)) return api_fail(DLM_EINVAL, kUnaligned);
   const PagedKV c = kv_of(cache);
   const int64_t row = (int64_t)c.Hkv * c.Dh;
   if (const char* why = rows_problem(k, k_stride, row, c.esize))
@@ -188,6 +195,8 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
   if (n_tokens == 0) return DLM_OK;
   if (!q || !o || !cu_q || !ctx_lens || !block_table || !workspace)
     return api_fail(DLM_EINVAL, "paged_attention: NULL pointer argument");
+  if (!aligned(lse, 4) || !aligned(cu_q, 4) || !aligned(ctx_lens, 4) || !aligned(block_table, 4))
+    return api_fail(DLM_EINVAL, kUnaligned);
   if (!aligned(workspace, 256))
     return api_fail(DLM_EINVAL, "paged_attention: the workspace is not 256-byte aligned");
   const PagedKV c = kv_of(cache);

@@ -18,6 +18,21 @@
 // halves, rows / 8 groups, 1 page): whatever the page size (>= 8), a 128-key
 // tile in shared memory is [16 groups of 8 rows][half][8 rows][128 bytes], with
 // one stride between 8-row groups, which is what the MMA descriptors need.
+//
+// What bounds it (32 query / 8 KV heads x 128 unless said otherwise):
+//   single tokens of 61 sequences over 1024..4096 keys: HBM, 655 MB in 121 us, 5.4
+//   TB/s; range, first pages and first tile take 7 us of it, the join 3;
+//   canvases of 32 over 32768 keys: HBM, 540 MB in 107 us, 5.0 TB/s;
+//   chunks of up to 4096 over up to 8192 keys, causal: the softmax, 1.33 TFLOP in 1262
+//   us, 1.06 PFLOP/s (1.45 ms where calls follow each other and the power limit
+//   lowers the clock).  A pair of 128 x 128 tiles takes 3900 cycles, 1025 of them
+//   tensor work and 2090 the exponential unit's: a warp by itself needs 1950 for its
+//   128 exponentials a lane, with their loads from and stores to tensor memory (the
+//   unit alone 1050), and the two warps of a scheduler side by side need no less
+//   than in turns;
+//   finished blocks of 256, 16 / 4 heads x 64, 700..1800 new tokens of 3 sequences: the
+//   same, 31.6 GFLOP in 76 us, 11 of them before the first P;
+//   a canvas of 32 over 2048 keys: latency, 17.7 us.
 #include "paged_attn.cuh"
 
 namespace dlm {
@@ -43,10 +58,12 @@ template <int DH>
 __device__ __forceinline__ uint32_t col_p(int i) {
   return DH == 64 ? kColO + 128 + i * 64 : i * kKeys + 64;
 }
-// cost of an item beside its keys, in keys: loading Q, the first S, the epilogue
+// Cost of an item beside its keys, in keys: loading Q, the first S, the epilogue.
+// Finished blocks of 256 tokens (16 / 4 heads x 64), causal chunks of up to 4096 (32 / 8
+// x 128), us: 32 keys 77.7 and 1285, 64 76.6 and 1279, 128 74.8 and 1269, 256 76.8 and 1243.
 constexpr int kItemCost = 128;
-// key tiles of a piece when there is little work (one: the join costs more than
-// the second tile)
+// Key tiles of a piece when there is little work.  A canvas of 32 over 2048 keys
+// (32 / 8 heads x 128), with the join: one tile 18.5 us (more to join), two 17.7, four 19.3.
 constexpr int kMinTiles = 2;
 // the running reference of a row moves only when its maximum passes it by
 // more than this (log2 units): P stays below 2^8, O is rarely rescaled
@@ -682,7 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The two row tiles (halves) take turns at the exponentials, each warp with
       // the one that shares its scheduler.  Left alone they fall into step, both
       // at the exponential unit and then both at the tensor core (chunks of up to
-      // 4096 tokens, 32 / 8 heads x 128: 1375 us against 1298 in turns).
+      // 4096 tokens, 32 / 8 heads x 128: 1350 us against 1262 in turns).  A turn
+      // is passed 32 keys before its end, about as long as the passing takes (at
+      // the end: 1282; after 64 of 128 keys: 1274; finished blocks of 256 tokens, 16 / 4
+      // heads x 64: 75.6, 77.1 and 77.1).
       const int turns = min(c0, c1);
       auto take_turn = [&](int x) {
         if (x >= turns) return true;
@@ -792,12 +812,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
             exp32(ra, wa);
             if (h == 0) tmem_ld32_nowait(s_col + 64, ra);
+            if (h == 1) pass_turn(x);
             exp32(rb, wb);
             if (h == 0) {
               tmem_ld32_nowait(s_col + 96, rb);
               tmem_wait_ld();
             }
-            if (h == 1) pass_turn(x);
             tmem_st16_u(p_col + h * 32, wa);
             tmem_st16_u(p_col + h * 32 + 16, wb);
             tmem_wait_st();

@@ -9,6 +9,11 @@
 // Q and the K and V tiles come by cp.async, the next tile during this one's
 // arithmetic.  Work is cut into equal ranges over all CTAs and joined as in the
 // bf16 kernel, so that a few short sequences still spread over the GPU.
+//
+// Bound by latency at the float32 model's sizes (4 heads x 64, 9 chunks of up to 96
+// tokens over up to 500 keys, causal, 0.12 GFLOP: 23.3 us a call with the join, of
+// which the range, the first tile and the join take about 12), by shared-memory
+// loads at larger ones.
 #include "paged_attn.cuh"
 
 namespace dlm {

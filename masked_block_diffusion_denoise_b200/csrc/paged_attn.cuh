@@ -219,7 +219,7 @@ __device__ void find_range(const Params& p, int key_tile, int item_cost, int min
     return max(1, (tiles(n, ctx, j) + min_tiles - 1) / min_tiles);
   };
   if (tid < 4) start[tid] = stop[tid] = 0;
-  // a sequence's cost, and its pieces unless its keys alone make more than the grid
+  // a sequence's cost, and its pieces unless its keys or items alone make more than the grid
   const long long few = (long long)gridDim.x * min_tiles * key_tile;
   longlong2 own = make_longlong2(0, 0), sum;
   for (int b = b0; b < b1; ++b) {
@@ -228,7 +228,8 @@ __device__ void find_range(const Params& p, int key_tile, int item_cost, int min
     const SeqCost s(n, ctx, pp, p.block, item_cost);
     const long long c = s.cum(s.items);
     own.x += c;
-    if ((c - (long long)s.items * item_cost) * p.Hkv > few || own.y > gridDim.x)
+    if ((c - (long long)s.items * item_cost) * p.Hkv > few || own.y > gridDim.x ||
+        s.items > (int)gridDim.x)
       own.y = gridDim.x + 1;
     else
       for (int j = 0; j * pp < n; ++j) own.y += pieces(n, ctx, j);
@@ -541,10 +542,11 @@ inline Params make_params(const PagedAttn& a, int ctas) {
   return p;
 }
 
-// `rows`: of a slot at most (the second row tile's begin at kSlotRows / 2).  With few rows altogether (n_tokens x n_heads up to
-// 16384) a row per warp, so that more SMs join; else four, so that the chains of
-// loads are fewer (canvas of 32 tokens, 32 heads: 22.4 us against 18.8 for the call;
-// chunks of up to 4096: the other way round, 15 us more).
+// `rows`: of a slot at most (the second row tile's begin at kSlotRows / 2).  With few
+// rows altogether (n_tokens x n_heads up to 16384) a row per warp, so that more SMs
+// join; else four, so that there are fewer blocks, each a chain of loads (attention
+// and join of a canvas of 32 tokens x 32 heads: 18.8 us with one row, 20.8 with four;
+// float32 chunks of up to 96 tokens x 4 heads: 24.0 and 28.7).
 template <typename T, int DH>
 cudaError_t launch_join(const Params& p, int ctas, int rows, cudaStream_t st) {
   if (p.T <= p.npos) rows = min(rows, p.T * p.G);   // one row tile at most

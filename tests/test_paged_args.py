@@ -71,6 +71,22 @@ def test_resize_ranges(i, value):
     refused(dlm.dlm_paged_resize, *args)
 
 
+@pytest.mark.parametrize("i", [0, 1, 2, 4, 7, 9, 10, 11, 12])
+def test_resize_unaligned(i):
+    args = [A, A, A, 2, A, 4, 16, A, 16, A, A, A, A, 8]
+    args[i] = A + (4 if i == 12 else 2)
+    refused(dlm.dlm_paged_resize, *args)
+
+
+def test_other_calls_unaligned():
+    refused(dlm.dlm_paged_kv_write, cache(), A, A, A + 4, 4)
+    for i in (3, 4, 5):
+        args = [cache(), A, A, A, A, A, 8, 1, 4, 4, 1]
+        args[i] += 2
+        refused(dlm.dlm_paged_attention, *args, Work(1 << 30))
+    refused(dlm.dlm_paged_attention, cache(), A, A, A, A, A, 8, 1, 4, 4, 1, Work(1 << 30), lse=A + 1)
+
+
 def test_write_refusals():
     c = cache()
     w = dlm.dlm_paged_kv_write
