@@ -458,7 +458,7 @@ int dlm_paged_attention_workspace(const dlm_paged_cache *cache, int n_heads, siz
  *            1: causal; c > 1: causal between blocks of c positions (the
  *            clean pass over finished blocks): the row at position p sees
  *            keys below min(ctx, (p / c + 1) * c)
- *   scale    of the scores; 0 means 1 / sqrt(head_dim)
+ *   scale    of the scores, at most 1e30; 0 means 1 / sqrt(head_dim)
  *   o        [n_tokens][n_heads][head_dim], rows o_stride elements apart
  *   lse      float32 [n_tokens][n_heads], or NULL: log of the sum of the
  *            exponentials of the scaled scores

@@ -188,10 +188,10 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
   if (const char* why = cache_problem(cache)) return api_fail(DLM_EINVAL, why);
   if (const char* why = heads_problem(cache, n_heads)) return api_fail(DLM_EINVAL, why);
   if (n_tokens < 0 || batch < 1 || batch > kPagedMaxBatch || table_width < 1 || mask_block < 0 ||
-      !(scale >= 0.f) || !(scale <= 3.0e38f))
+      !(scale >= 0.f) || !(scale <= 1e30f))
     return api_fail(DLM_EINVAL,
                     "paged_attention: need n_tokens >= 0, 1 <= batch <= 4096, table_width >= 1, "
-                    "mask_block >= 0 and a finite scale >= 0");
+                    "mask_block >= 0 and 0 <= scale <= 1e30");
   if (n_tokens == 0) return DLM_OK;
   if (!q || !o || !cu_q || !ctx_lens || !block_table || !workspace)
     return api_fail(DLM_EINVAL, "paged_attention: NULL pointer argument");

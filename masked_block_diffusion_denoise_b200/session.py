@@ -227,6 +227,9 @@ class PagedCache:
     def resize(self, new_lens: torch.Tensor, stream=None) -> None:
         """Lengths (int32 [batch], device) that the sequences are to have; a
         sequence that does not get its pages keeps its length (see .lens)."""
+        if (new_lens.dtype != torch.int32 or new_lens.shape != (self.batch,) or
+                not new_lens.is_contiguous()):
+            raise ValueError("resize: new_lens is int32 [batch] without gaps")
         dlm_paged_resize(self.lens, new_lens, self.lens, self.batch, self.table, self.width,
                          self.page_size, self.free, self.k.shape[0], self.n_free, self.n_free,
                          self.cu, self.slots, self.max_new, stream=stream)
@@ -236,32 +239,37 @@ class PagedCache:
         in sequence order (rows may be strided)."""
         if k.shape[0] != v.shape[0] or k.shape[0] > self.max_new:
             raise ValueError("write: k and v have one row per new token, at most max_new")
-        self._rows(k, "k")
-        self._rows(v, "v")
-        dlm_paged_kv_write(self.c, k, v, self.slots, k.shape[0], k_stride=k.stride(0),
-                           v_stride=v.stride(0), stream=stream)
+        heads = self.k.shape[1]
+        dlm_paged_kv_write(self.c, k, v, self.slots, k.shape[0], stream=stream,
+                           k_stride=self._stride(k, heads, "k"),
+                           v_stride=self._stride(v, heads, "v"))
 
     def attend(self, q: torch.Tensor, mask_block: int, out: Optional[torch.Tensor] = None,
                lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Attention of the new tokens' queries [rows][n_heads][head_dim] over their
         sequences; mask_block 0 (every key), 1 (causal) or a block length."""
-        self._rows(q, "q")
         if out is None:
-            out = torch.empty((q.shape[0], self.n_heads, self.k.shape[3]), dtype=self.dtype,
-                              device=self.device)
-        self._rows(out, "out")
-        if out.shape != q.shape or q.shape[1] != self.n_heads:
-            raise ValueError("attend: q and out are [rows][n_heads][head_dim]")
+            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+        if out.shape != q.shape:
+            raise ValueError("attend: out has q's shape")
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or
+                                not lse.is_contiguous()):
+            raise ValueError("attend: lse is float32 [rows][n_heads] without gaps")
         dlm_paged_attention(self.c, q, out, self.cu, self.lens, self.table, self.width, self.batch,
                             q.shape[0], self.n_heads, mask_block, self.work, lse=lse,
-                            q_stride=q.stride(0), o_stride=out.stride(0), stream=stream)
+                            q_stride=self._stride(q, self.n_heads, "q"),
+                            o_stride=self._stride(out, self.n_heads, "out"), stream=stream)
         return out
 
     def check(self, stream=None) -> None:
         dlm_paged_check(stream)
 
-    def _rows(self, t: torch.Tensor, what: str) -> None:
-        if (t.dtype != self.dtype or t.dim() != 3 or t.shape[2] != self.k.shape[3] or
-                t.stride(2) != 1 or t.stride(1) != t.shape[2]):
-            raise ValueError("%s: [rows][heads][head_dim] of the cache's type, heads without gaps"
-                             % what)
+    def _stride(self, t: torch.Tensor, heads: int, what: str) -> int:
+        """Elements between rows of [rows][heads][head_dim] (0: there is one at most)."""
+        dim = self.k.shape[3]
+        if (t.dtype != self.dtype or t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim) or
+                t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim) or
+                (t.shape[0] > 1 and t.stride(0) < heads * dim)):
+            raise ValueError("%s: [rows][heads][head_dim] of the cache's type, heads without gaps "
+                             "and rows that do not overlap" % what)
+        return t.stride(0) if t.shape[0] > 1 else 0

@@ -648,10 +648,30 @@ def test_paged_cache_object(dtype, dim):
             at += new[b]
         host = want
     assert pc.lens.tolist() == [0, 78] and int(pc.n_free) == 40 - OP.pages(78, 16)
+    pc.attend(q, 1, lse=torch.empty(q.shape[:2], device="cuda"))
     with pytest.raises(ValueError):
-        pc.write(k.float().double(), v)
+        pc.write(k.double(), v.double())
+    with pytest.raises(ValueError):
+        pc.write(k[:, :1], v[:, :1])                       # too few heads
+    with pytest.raises(ValueError):
+        pc.write(k[:1].expand(4, kv, dim), v[:1].expand(4, kv, dim))   # one row four times
     with pytest.raises(ValueError):
         pc.attend(q[:, :2], 1)
+    with pytest.raises(ValueError):
+        pc.attend(q, 1, lse=torch.empty((1, 1), device="cuda"))
+    with pytest.raises(ValueError):
+        pc.attend(q, 1, out=torch.empty((2, heads, dim), device="cuda").to(pc.dtype))
+    with pytest.raises(ValueError):
+        pc.resize(torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        pc.resize(i32([1, 2, 3]))
+    # one row from a strided view: its row stride is not asked for
+    x = torch.randn((1, 3 * kv, dim), generator=g, device="cuda").to(pc.dtype)[:, kv:2 * kv]
+    pc.resize(i32([0, 79]))
+    pc.write(x, x)
+    page, off = pc.table[1, 78 // 16], 78 % 16
+    pc.check()
+    assert torch.equal(pc.k[page, :, off], x[0]) and torch.equal(pc.v[page, :, off], x[0])
 
 
 def test_captured_step_follows_device_lengths():

@@ -112,7 +112,7 @@ def test_attention_refusals(i, value):
 
 
 @pytest.mark.parametrize("kw", [dict(scale=-1.0), dict(scale=float("nan")),
-                                dict(scale=float("inf")), dict(q_stride=508),
+                                dict(scale=float("inf")), dict(scale=1e31), dict(q_stride=508),
                                 dict(q_stride=516), dict(o_stride=100)])
 def test_attention_options_refused(kw):
     refused(dlm.dlm_paged_attention, cache(), A, A, A, A, A, 8, 1, 4, 4, 1, Work(1 << 30), **kw)
