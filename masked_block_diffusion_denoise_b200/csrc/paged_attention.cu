@@ -20,9 +20,9 @@
 // one stride between 8-row groups, which is what the MMA descriptors need.
 //
 // What bounds it (32 query / 8 KV heads x 128 unless said otherwise):
-//   single tokens of 61 sequences over 1024..4096 keys: HBM, 655 MB in 121 us, 5.4
-//   TB/s; range, first pages and first tile take 7 us of it, the join 3;
-//   canvases of 32 over 32768 keys: HBM, 540 MB in 107 us, 5.0 TB/s;
+//   single tokens of 61 sequences over 1024..4096 keys: HBM, 655 MB in 119 us, 5.5
+//   TB/s; range, first pages and first tile take 7 us of it;
+//   canvases of 32 over 32768 keys: HBM, 540 MB in 104 us, 5.2 TB/s;
 //   chunks of up to 4096 over up to 8192 keys, causal: the softmax, 1.33 TFLOP in 1262
 //   us, 1.06 PFLOP/s (1.45 ms where calls follow each other and the power limit
 //   lowers the clock).  A pair of 128 x 128 tiles takes 3900 cycles, 1025 of them
@@ -31,8 +31,9 @@
 //   unit alone 1050), and the two warps of a scheduler side by side need no less
 //   than in turns;
 //   finished blocks of 256, 16 / 4 heads x 64, 700..1800 new tokens of 3 sequences: the
-//   same, 31.6 GFLOP in 76 us, 11 of them before the first P;
-//   a canvas of 32 over 2048 keys: latency, 17.7 us.
+//   same, 31.6 GFLOP in 73 us, 11 of them before the first P;
+//   a canvas of 32 over 2048 keys: latency, 16.5 us: range 2.6, its item and page ids 1.6,
+//   first tile 0.9, first P 1.9, results 1.3, their stores and the join.
 #include "paged_attn.cuh"
 
 namespace dlm {
@@ -604,13 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             w0 *= inv;
             w1 *= inv;
           }
-          const size_t prow =
-              ((size_t)blockIdx.x * 2 + it.slot) * kSlotRows + (pair ? i * kRows : 0) + row;
+          const size_t slot = (size_t)blockIdx.x * 2 + it.slot;
+          const int prow = (pair ? i * kRows : 0) + row;
           const int64_t grow = (int64_t)it.row0 + pos;
           const int head = it.g * p.G + rh;
           if (__any_sync(0xffffffffu, live)) {
             uint4* dst_o = reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + grow * p.o_stride + (int64_t)head * DH);
-            float4* dst_p = reinterpret_cast<float4*>(p.part + prow * DH);
             // 16 columns at a time: little code, which runs once per item
 #pragma unroll 1
             for (int y = 0; y < DH / 16; ++y) {
@@ -645,11 +645,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               } else if (live) {
 #pragma unroll
                 for (int z = 0; z < 4; ++z)
-                  dst_p[y * 4 + z] = make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+                  *reinterpret_cast<float4*>(p.part + part_at<__nv_bfloat16, DH>(slot, prow, y * 16 + z * 4)) =
+                      make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
               }
             }
             if (live && !whole)
-              p.ml[prow] = make_float2(m, l);
+              p.ml[slot * kSlotRows + prow] = make_float2(m, l);
             else if (live && p.lse != nullptr)
               p.lse[(size_t)grow * p.H + head] =
                   l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;

@@ -77,7 +77,7 @@ struct Params {
   void* o;
   int64_t o_stride;
   float* lse;
-  float* part;         // [cta][2][kSlotRows][Dh]
+  float* part;         // [cta][2][kSlotRows x Dh], order: part_at
   float2* ml;          // [cta][2][kSlotRows]
   Meta* meta;          // [cta]
   int* err;
@@ -390,115 +390,115 @@ struct Walker {
   }
 };
 
+// Where column `col` of row `row` of a partial lies, in floats.  The bf16 kernel's
+// writers hold a row per lane: four columns of all rows, then the next four, so
+// that their 16-byte stores fill whole lines (row after row they touched 32 lines
+// each: canvas of 32 tokens, 32 heads 17.7 us instead of 16.6 for the call).  The
+// float32 kernel's threads hold a row's columns side by side: row after row (22.8 us
+// for its chunks of up to 96 tokens, 23.7 the other way).
+template <typename T, int DH>
+__device__ __forceinline__ size_t part_at(size_t slot, int row, int col) {
+  if (std::is_same<T, float>::value) return (slot * kSlotRows + row) * DH + col;
+  return ((slot * (DH / 4) + (col >> 2)) * kSlotRows + row) * 4 + (col & 3);
+}
+
 // Joins the partials of an item that starts in CTA c: c's own, then those of
-// c + 1, ... up to the CTA where it ends, in that order.  A warp joins
-// R rows at once, lane = DH / 32 columns: the partials' maxima and
-// sums 32 at a time in the lanes, then their rows in batches of independent
-// loads (the join is a chain of loads, so it is the number of links that counts).
-template <typename T, int DH, int R>
+// c + 1, ... up to the CTA where it ends, in that order.  A warp takes 8 rows x 16
+// columns, four columns a lane, and kBatch partials at a time: their maxima,
+// sums and columns are all loaded before any is used, since the join is a chain
+// of loads and it is the number of links that counts.
+template <typename T, int DH>
 __global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_ctas) {
-  constexpr int E = DH / 32, kJoinRows = 8 * R;
-  using Vec = typename std::conditional<
-      E == 4, float4, typename std::conditional<E == 2, float2, float>::type>::type;
+  constexpr int kRowWarps = DH / 16, kGroups = 8 / kRowWarps, kBatch = 8;
   constexpr int kTileRows = kSlotRows / 2;
   pdl_wait_then_release();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Meta me = p.meta[c];
-  // rows r0 + 8 u of row tile `tile`; those in use are the tile's first ones
-  const int tile = blockIdx.y * kJoinRows / kTileRows;
-  const int r0 = blockIdx.y * kJoinRows + warp;
-  const int used = tile * kTileRows + min(p.npos, me.npos - tile * p.npos) * p.G;
-  if (!me.tail || r0 >= used) return;
-  float m[R], l[R], acc[R][E];
-#pragma unroll
-  for (int u = 0; u < R; ++u) {
-    m[u] = -CUDART_INF_F;
-    l[u] = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[u][e] = 0.f;
-  }
-  bool ends = false;
-  for (int k0 = c; k0 < n_ctas && !ends; k0 += 32) {
+  // the CTAs behind c, 32 at a time in the lanes: those with a partial of the item,
+  // and up to which one it goes
+  uint32_t heads, upto;
+  bool ends;
+  auto look = [&](int k0) {
     const int k = k0 + lane;
-    const bool next = k < n_ctas && k > c;
-    const bool here = k == c || (next && p.meta[k].head != 0);
-    const uint32_t stops = __ballot_sync(0xffffffffu, next && p.meta[k].head_ends != 0);
-    ends = stops != 0;
-    const int n = ends ? __ffs(stops) : min(32, n_ctas - k0);   // partials of this batch
-    float w[R];
-    {
-      float2 v[R];
+    const bool in = k < n_ctas && k > c;
+    const int head = in ? p.meta[k].head : 0, last = in ? p.meta[k].head_ends : 0;
+    const uint32_t stops = __ballot_sync(0xffffffffu, last != 0);
+    ends = stops != 0 || k0 + 32 >= n_ctas;
+    upto = stops != 0 ? 0xffffffffu >> (32 - __ffs(stops)) : 0xffffffffu;
+    heads = (__ballot_sync(0xffffffffu, head != 0) | (k0 == c ? 1u : 0u)) & upto;
+  };
+  // rows in use of row tile `tile`: its first ones
+  auto used = [&](int tile) { return min(p.npos, me.npos - tile * p.npos) * p.G; };
+  // blocks without rows leave before they look further (the first one has some,
+  // and looks while it waits for `me`)
+  const int first = blockIdx.y * kGroups * 8;
+  if (first > 0 && (!me.tail || (!me.pair && first >= used(0)))) return;
+  look(c);
+  if (!me.tail) return;
+  const int col = (warp % kRowWarps) * 16 + (lane >> 3) * 4;
+  for (int g = blockIdx.y * kGroups + warp / kRowWarps; g < kSlotRows / 8;
+       g += gridDim.y * kGroups) {
+    const int row = g * 8 + (lane & 7), tile = row / kTileRows, x = row - tile * kTileRows;
+    const bool live = x < used(tile);
+    if (!__any_sync(0xffffffffu, live)) continue;
+    float m = -CUDART_INF_F, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = c;; k0 += 32) {
+      if (k0 > c || g >= (int)gridDim.y * kGroups) look(k0);   // (done for the first group)
+      for (uint32_t rest = heads; rest != 0;) {
+        float2 v[kBatch];
+        float4 y[kBatch];
+        float bm = m;
 #pragma unroll
-      for (int u = 0; u < R; ++u)
-        v[u] = here && lane < n && r0 + 8 * u < used ? p.ml[((size_t)k * 2 + (k == c)) * kSlotRows + r0 + 8 * u]
-                                : make_float2(-CUDART_INF_F, 0.f);
+        for (int u = 0; u < kBatch; ++u) {
+          v[u] = make_float2(-CUDART_INF_F, 0.f);
+          if (rest == 0 || !live) continue;
+          const int k = k0 + __ffs(rest) - 1;
+          rest &= rest - 1;
+          const size_t slot = (size_t)k * 2 + (k == c);
+          v[u] = p.ml[slot * kSlotRows + row];
+          y[u] = *reinterpret_cast<const float4*>(p.part + part_at<T, DH>(slot, row, col));
+        }
+        if (!live) rest = 0;
 #pragma unroll
-      for (int u = 0; u < R; ++u) {
-        float bm = v[u].x;
+        for (int u = 0; u < kBatch; ++u) bm = fmaxf(bm, v[u].x);
+        const float base = bm == -CUDART_INF_F ? 0.f : bm;   // no key seen so far
+        const float old = fast_exp2(m - base);
+        l *= old;
+        acc.x *= old;
+        acc.y *= old;
+        acc.z *= old;
+        acc.w *= old;
+        m = bm;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
-        const float m_new = fmaxf(m[u], bm);
-        const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // no key seen so far
-        const float old = fast_exp2(m[u] - base);
-        w[u] = fast_exp2(v[u].x - base);
-        float bl = w[u] == 0.f ? 0.f : w[u] * v[u].y;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) bl += __shfl_xor_sync(0xffffffffu, bl, d);
-        l[u] = l[u] * old + bl;
-        m[u] = m_new;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[u][e] *= old;
-      }
-    }
-    constexpr int kB = R == 1 ? 8 : 4;
-    for (int s = 0; s < n; s += kB) {
-      Vec y[R][kB];
-      float ws[R][kB];
-#pragma unroll
-      for (int x = 0; x < kB; ++x) {
-        const size_t row =
-            ((size_t)(k0 + s + x) * 2 + (k0 + s + x == c)) * kSlotRows + r0;
-#pragma unroll
-        for (int u = 0; u < R; ++u) {
-          ws[u][x] = __shfl_sync(0xffffffffu, w[u], (s + x) & 31);
-          if (s + x >= n) ws[u][x] = 0.f;
-          // (a weight of 0: no partial, or rows behind the item's last)
-          if (ws[u][x] != 0.f)
-            y[u][x] = *reinterpret_cast<const Vec*>(p.part + (row + 8 * u) * DH + lane * E);
+        for (int u = 0; u < kBatch; ++u) {
+          const float w = fast_exp2(v[u].x - base);
+          if (w == 0.f) continue;   // no key of this row there
+          l = fmaf(w, v[u].y, l);
+          acc.x = fmaf(w, y[u].x, acc.x);
+          acc.y = fmaf(w, y[u].y, acc.y);
+          acc.z = fmaf(w, y[u].z, acc.z);
+          acc.w = fmaf(w, y[u].w, acc.w);
         }
       }
-#pragma unroll
-      for (int x = 0; x < kB; ++x)
-#pragma unroll
-        for (int u = 0; u < R; ++u)
-          if (ws[u][x] != 0.f) {
-            const float* f = reinterpret_cast<const float*>(&y[u][x]);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[u][e] = fmaf(ws[u][x], f[e], acc[u][e]);
-          }
+      if (ends) break;
     }
-  }
-#pragma unroll
-  for (int u = 0; u < R; ++u) {
-    if (r0 + 8 * u >= used) continue;
-    const int x = r0 + 8 * u - tile * kTileRows;
+    if (!live) continue;
     const int rp = div_g(p, x), rh = x - rp * p.G, pos = tile * p.npos + rp;
-    const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t grow = (int64_t)me.row0 + pos;
     const int head = me.g * p.G + rh;
-    T* dst = (T*)p.o + grow * p.o_stride + (int64_t)head * DH + lane * E;
+    T* dst = (T*)p.o + grow * p.o_stride + (int64_t)head * DH + col;
     if constexpr (std::is_same<T, float>::value) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) dst[e] = acc[u][e] * inv;
+      *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     } else {
-#pragma unroll
-      for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<__nv_bfloat162*>(dst + e) =
-            __floats2bfloat162_rn(acc[u][e] * inv, acc[u][e + 1] * inv);
+      __nv_bfloat162 r[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                             __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
+      *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(r);
     }
-    if (p.lse != nullptr && lane == 0)
+    if (p.lse != nullptr && col == 0)
       p.lse[(size_t)grow * p.H + head] =
-          l[u] == 0.f ? -CUDART_INF_F : (m[u] + log2f(l[u])) * 0.69314718055994531f;
+          l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -542,17 +542,20 @@ inline Params make_params(const PagedAttn& a, int ctas) {
   return p;
 }
 
-// `rows`: of a slot at most (the second row tile's begin at kSlotRows / 2).  With few
-// rows altogether (n_tokens x n_heads up to 16384) a row per warp, so that more SMs
-// join; else four, so that there are fewer blocks, each a chain of loads (attention
-// and join of a canvas of 32 tokens x 32 heads: 18.8 us with one row, 20.8 with four;
-// float32 chunks of up to 96 tokens x 4 heads: 24.0 and 28.7).
+// `rows`: of a slot at most.  Blocks per CTA's item for half as many rows again as a
+// sequence's tokens make on average, so that few are launched for nothing; longer
+// items loop.  (us a call: single tokens of 61 sequences, 4 rows an item, blocks for 256
+// rows 121.2, for 8 119.4; canvases of 32 over 32768 keys, 128 rows, for 256 105.0, for 128
+// 103.3; one canvas of 32 over 2048, for all 128 16.5, for 64 and less 21.0; float32 chunks
+// of 1..96 tokens, for 64 rows 22.5, for their mean 23.8; causal chunks of up to 4096: no
+// difference.)
 template <typename T, int DH>
 cudaError_t launch_join(const Params& p, int ctas, int rows, cudaStream_t st) {
-  if (p.T <= p.npos) rows = min(rows, p.T * p.G);   // one row tile at most
-  if ((long long)p.T * p.H <= 16384)
-    return launch_pdl(paged_join_kernel<T, DH, 1>, dim3(ctas, (rows + 7) / 8), dim3(256), 0, st, p, ctas);
-  return launch_pdl(paged_join_kernel<T, DH, 4>, dim3(ctas, (rows + 31) / 32), dim3(256), 0, st, p,
+  constexpr int kBlockRows = 8 * (8 / (DH / 16));
+  const long long tokens = min((long long)p.T, (3ll * p.T + 2 * p.B - 1) / (2 * p.B));
+  rows = (int)min((long long)rows, tokens * p.G);
+  const int blocks = (rows + kBlockRows - 1) / kBlockRows;
+  return launch_pdl(paged_join_kernel<T, DH>, dim3(ctas, blocks), dim3(256), 0, st, p,
                     ctas);
 }
 
