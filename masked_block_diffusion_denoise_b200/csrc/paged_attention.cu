@@ -64,7 +64,8 @@ __device__ __forceinline__ uint32_t col_p(int i) {
 // x 128), us: 32 keys 77.7 and 1285, 64 76.6 and 1279, 128 74.8 and 1269, 256 76.8 and 1243.
 constexpr int kItemCost = 128;
 // Key tiles of a piece when there is little work.  A canvas of 32 over 2048 keys
-// (32 / 8 heads x 128), with the join: one tile 18.5 us (more to join), two 17.7, four 19.3.
+// (32 / 8 heads x 128), with the join: one tile 17.4 us (more to join), two 16.5; four 1.6 us
+// more than two.
 constexpr int kMinTiles = 2;
 // the running reference of a row moves only when its maximum passes it by
 // more than this (log2 units): P stays below 2^8, O is rarely rescaled

@@ -513,6 +513,10 @@ def reference(p, q, new, heads, block):
     ("bf16", 66, 2, 64, 32, [(500, 40), (301, 7)], 1),
     ("bf16", 20, 4, 64, 16, [(700, 30), (1301, 27)] * 3, 0),
     ("bf16", 33, 1, 128, 8, [(780, 6)], 0),      # joined rows of a second row tile
+    # one long chunk among single tokens: its rows are many times the mean
+    ("bf16", 16, 4, 128, 16, [(40, 1)] * 30 + [(20000, 64)] + [(200, 1)] * 30, 0),
+    ("bf16", 16, 4, 64, 16, [(40, 1)] * 30 + [(20000, 50)] + [(200, 1)] * 30, 1),
+    ("f32", 8, 1, 64, 16, [(40, 1)] * 30 + [(9000, 17)] + [(200, 1)] * 30, 0),
     ("f32", 4, 2, 64, 32, [(6000, 70), (300, 300)], 1),
     ("f32", 6, 1, 128, 16, [(1500, 257)], 0),
 ])
