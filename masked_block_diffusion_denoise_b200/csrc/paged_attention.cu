@@ -768,10 +768,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = fmax3f(m4[0], m4[1], fmaxf(m4[2], m4[3]));
           }
           mx *= p.scale_log2;
-          const bool move = __any_sync(0xffffffffu, mx > m_run + kRescaleLog2);
-          const float m_new = move ? fmaxf(m_run, mx) : m_run;
+          // A row's reference follows its own scores alone.  Lanes that hold no row score
+          // whatever lies in their rows of Q and in the slots behind the sequence, and other
+          // rows see other keys: a reference shared by the warp would let those decide how
+          // this row's P is scaled when it is rounded to bf16.  The vote is only for the
+          // rescaling of O, which the warp's loads and stores do together.
+          const bool rises = mx > m_run + kRescaleLog2;
+          const bool move = __any_sync(0xffffffffu, rises && live);
+          const float m_new = rises ? mx : m_run;
           const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // no key seen yet
-          const float alpha = move ? fast_exp2(m_run - base) : 1.f;
+          const float alpha = rises ? fast_exp2(m_run - base) : 1.f;
           if (x > 0 && move) {
 #pragma unroll 1
             for (int y = 0; y < DH / 32; ++y) {

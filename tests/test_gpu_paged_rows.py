@@ -1,0 +1,92 @@
+"""Paged attention, row by row: what a row's result depends on and what it
+does not (other rows, slots that hold no token, what ran before)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - collected on CPU-only hosts
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from test_gpu_paged import Paged, ready
+
+# Sequences of several key tiles a CTA: a row's softmax reference has earlier
+# tiles to fall behind.  (heads, kv heads): G 4; 3, 5 and 7 do not divide a
+# row tile of 128, whose last rows then hold no query at all.
+GROUPS = [(8, 2), (6, 2), (10, 2), (14, 2)]
+LENGTHS = [600 + 37 * b for b in range(60)]
+
+
+@pytest.mark.parametrize("heads,kv", GROUPS)
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("n", [1, 3])
+def test_unused_slots_do_not_reach_a_result(heads, kv, dim, n):
+    """Slots behind a sequence hold large finite values, or infinities: the
+    same bits as with zeros there."""
+    outs = []
+    for junk in (0.0, 1e4, -3e38, float("inf")):
+        p = Paged("bf16", kv, dim, 64, LENGTHS, seed=5, junk=junk)
+        q = ready(p, [n] * len(LENGTHS), heads, 5)
+        o, lse, _ = p.attend(q, [n] * len(LENGTHS), heads, 1)
+        outs.append((o, lse))
+    for o, lse in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
+@pytest.mark.parametrize("heads,kv", GROUPS)
+@pytest.mark.parametrize("block", [0, 1])
+def test_other_sequences_queries_do_not_reach_a_row(heads, kv, block):
+    p = Paged("bf16", kv, 128, 16, LENGTHS, seed=6, junk=0.0)
+    new = [1 + b % 3 for b in range(len(LENGTHS))]
+    q = ready(p, new, heads, 6)
+    o, lse, cu = p.attend(q, new, heads, block)
+    loud = q.clone()
+    for b in range(1, len(new), 2):
+        loud[cu[b]:cu[b + 1]] *= 64
+    o2, lse2, _ = p.attend(loud, new, heads, block)
+    for b in range(0, len(new), 2):
+        rows = slice(cu[b], cu[b + 1])
+        assert torch.equal(o[rows], o2[rows]) and torch.equal(lse[rows], lse2[rows]), b
+
+
+@pytest.mark.parametrize("heads,kv,dim", [(8, 2, 128), (6, 2, 64), (4, 4, 128)])
+def test_other_rows_of_a_chunk_do_not_reach_a_row(heads, kv, dim):
+    """One position's query is 64 times as large; the keys that only the last
+    position sees are: the other rows' bits stay."""
+    ctx, n = 6000, 300
+    p = Paged("bf16", kv, dim, 16, [ctx], seed=7)
+    q = ready(p, [n], heads, 7)
+    o, lse, _ = p.attend(q, [n], heads, 1)
+    loud = q.clone()
+    loud[5] *= 64
+    loud[170] *= 64
+    o2, lse2, _ = p.attend(loud, [n], heads, 1)
+    rest = [i for i in range(n) if i not in (5, 170)]
+    assert torch.equal(o[rest], o2[rest]) and torch.equal(lse[rest], lse2[rest])
+    last = ctx - 1
+    p.kc[int(p.table[0, last // 16]), :, last % 16] *= 64
+    o3, lse3, _ = p.attend(q, [n], heads, 1)
+    assert torch.equal(o[:-1], o3[:-1]) and torch.equal(lse[:-1], lse3[:-1])
+
+
+@pytest.mark.parametrize("heads,kv", GROUPS)
+@pytest.mark.parametrize("dim", [128, 64])
+def test_same_bits_whatever_ran_before(heads, kv, dim):
+    """The same call after kernels that leave other values in shared and tensor
+    memory."""
+    p = Paged("bf16", kv, dim, 16, LENGTHS, seed=8, junk=0.0)
+    new = [1 + b % 2 for b in range(len(LENGTHS))]
+    q = ready(p, new, heads, 8)
+    big = Paged("bf16", 2, dim, 64, [3000, 900], seed=9)
+    bq = ready(big, [700, 900], 8, 9, spread=100.0)
+    a = torch.randn((4096, 4096), device="cuda", dtype=torch.bfloat16) * 1e3
+    o, lse, _ = p.attend(q, new, heads, 1)
+    for r in range(6):
+        if r % 2:
+            a @ a
+        else:
+            big.attend(bq * (r + 1), [700, 900], 8, 1)
+        o2, lse2, _ = p.attend(q, new, heads, 1)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
