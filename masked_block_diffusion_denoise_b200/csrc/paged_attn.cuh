@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_c
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           v[u] = make_float2(-CUDART_INF_F, 0.f);
+          y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (rest == 0 || !live) continue;
           const int k = k0 + __ffs(rest) - 1;
           rest &= rest - 1;
@@ -472,8 +473,10 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_c
         m = bm;
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
+          // A part without a key of this row has l and columns of 0.  None is passed
+          // over for a weight of 0: where every score was NaN the maximum is -inf and
+          // l is NaN, and that has to reach the result, as it does in an item that is not cut.
           const float w = fast_exp2(v[u].x - base);
-          if (w == 0.f) continue;   // no key of this row there
           l = fmaf(w, v[u].y, l);
           acc.x = fmaf(w, y[u].x, acc.x);
           acc.y = fmaf(w, y[u].y, acc.y);

@@ -1,6 +1,5 @@
 """Paged attention, row by row: what a row's result depends on and what it
 does not (other rows, slots that hold no token, what ran before)."""
-import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -90,3 +89,58 @@ def test_same_bits_whatever_ran_before(heads, kv, dim):
             big.attend(bq * (r + 1), [700, 900], 8, 1)
         o2, lse2, _ = p.attend(q, new, heads, 1)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# ---------------------------------------------------------------------------
+# NaN and infinities that a row does see
+# ---------------------------------------------------------------------------
+
+def set_key(p, b, j, cache, column, value):
+    """Element `column` of key j of sequence b (all KV heads), in the pages and beside them."""
+    (p.kc if cache == "k" else p.vc)[int(p.table[b, j // p.page]), :, j % p.page, column] = value
+    (p.k if cache == "k" else p.v)[b][j, :, column] = value
+
+
+KINDS = [("bf16", 128), ("bf16", 64), ("f32", 64), ("f32", 128)]
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("ctx,n", [(2500, 1), (100, 1), (40, 7), (3000, 40)])
+@pytest.mark.parametrize("block", [0, 1])
+def test_nan_in_a_query(dtype, dim, ctx, n, block):
+    """One head of one row holds a NaN: its result and lse are NaN however the work is
+    cut (2500 keys: over many CTAs; 100: in one), the others keep their bits."""
+    p = Paged(dtype, 2, dim, 16, [ctx, 30], seed=12)
+    q = ready(p, [n, 2], 8, 12)
+    o, lse, _ = p.attend(q, [n, 2], 8, block)
+    q[n // 2, 3, 7] = float("nan")
+    o2, lse2, _ = p.attend(q, [n, 2], 8, block)
+    assert torch.isnan(o2[n // 2, 3]).all() and torch.isnan(lse2[n // 2, 3])
+    o2[n // 2, 3], lse2[n // 2, 3] = o[n // 2, 3], lse[n // 2, 3]
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("cache,value", [("k", float("nan")), ("v", float("nan")),
+                                         ("v", float("inf")), ("v", -float("inf"))])
+@pytest.mark.parametrize("where", [3, 2000])
+def test_bad_key_far_below_the_maximum(dtype, dim, cache, value, where):
+    """A NaN or an infinity in a key whose neighbours' weights are 2^-200 of the others': a
+    part of the work with weight 0 in float32, and still not a finite result."""
+    ctx = 2500
+    p = Paged(dtype, 1, dim, 16, [ctx], seed=13)
+    lo = where // 400 * 400
+    p.k[0].zero_()
+    p.k[0][lo:lo + 400] = -200.0 / (1.4427 * dim ** 0.5)   # 1 . k / sqrt(dim) log2(e) = -200
+    p.put(p.table[0].cpu().numpy(), p.k[0], p.kc)
+    q = torch.ones((1, 4, dim), device="cuda").to(p.dtype)
+    o, lse, _ = p.attend(q, [1], 4, 1)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    set_key(p, 0, where, cache, 9, value)
+    o2, lse2, _ = p.attend(q, [1], 4, 1)
+    if cache == "k":
+        assert torch.isnan(o2).all() and torch.isnan(lse2).all()
+    else:
+        assert not torch.isfinite(o2[:, :, 9]).any()
+        rest = [c for c in range(dim) if c != 9]
+        assert torch.equal(o2[:, :, rest], o[:, :, rest]) and torch.equal(lse, lse2)
