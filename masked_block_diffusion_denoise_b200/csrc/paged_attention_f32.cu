@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_f32_kernel(co
 #pragma unroll
           for (int j = 0; j < KN; ++j) ps[(ty * 4 + i) * kLdP + tx + 16 * j] = s[i][j];
         __syncwarp();   // a row's P is written and read by one half-warp
-        // O += P V; in tiles with hidden keys a probability of 0 takes nothing
-        // from V (0 x infinity would be NaN)
+        // O += P V; in tiles with hidden keys a row takes nothing from the V of those
+        // (0 x infinity would be NaN).  Asked of the key, not of its probability: a seen
+        // key's may underflow to 0, and its V still counts if it is not finite
         auto pv = [&](auto hidden) {
 #pragma unroll 2
           for (int k = 0; k < BN; k += 4) {
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_f32_kernel(co
 #pragma unroll
                 for (int j = 0; j < DN / 2; ++j)
                   acc[i][j] = fma2(pack2(w[y], w[y]),
-                                   decltype(hidden)::value && w[y] == 0.f ? 0ull : b[y][j], acc[i][j]);
+                                   decltype(hidden)::value && k0 + k + y >= lim[i] ? 0ull : b[y][j], acc[i][j]);
             }
           }
         };

@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover - collected on CPU-only hosts
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
+from oracle import paged as OP
 from test_gpu_paged import Paged, ready
 
 # Sequences of several key tiles a CTA: a row's softmax reference has earlier
@@ -144,3 +145,55 @@ def test_bad_key_far_below_the_maximum(dtype, dim, cache, value, where):
         assert not torch.isfinite(o2[:, :, 9]).any()
         rest = [c for c in range(dim) if c != 9]
         assert torch.equal(o2[:, :, rest], o[:, :, rest]) and torch.equal(lse, lse2)
+def defined(p, q, new, heads, block):
+    """(o, lse) of every row from the keys that it sees, in float64 on the CPU,
+    with NaN and infinities going where the formula takes them."""
+    o = torch.zeros(q.shape, dtype=torch.float64)
+    lse = torch.full(q.shape[:2], -torch.inf, dtype=torch.float64)
+    row, g = 0, heads // p.kv
+    for b, n in enumerate(new):
+        k, v = p.k[b].double().cpu(), p.v[b].double().cpu()
+        for i in range(n):
+            m = OP.visible(p.ctx[b] - n + i, p.ctx[b], block)
+            for h in range(heads if m else 0):
+                s = k[:m, h // g] @ q[row, h].double().cpu() / p.dim ** 0.5
+                o[row, h] = torch.softmax(s, 0) @ v[:m, h // g]
+                lse[row, h] = torch.logsumexp(s, 0)
+            row += 1
+    return o, lse
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("ctx,n", [(150, 60), (2300, 30)])
+def test_rows_that_see_bad_keys(dtype, dim, bad, ctx, n):
+    """Keys with NaN or infinities in K and V among the chunk's own: a result is finite
+    exactly where the formula's is."""
+    p = Paged(dtype, 2, dim, 16, [ctx], seed=14)
+    q = ready(p, [n], 4, 14)
+    for j in range(ctx - 19, ctx, 7):
+        set_key(p, 0, j, "k", 9, bad)
+        set_key(p, 0, j, "v", 5, bad)
+    o, lse, _ = p.attend(q, [n], 4, 1)
+    ref, rl = defined(p, q, [n], 4, 1)
+    assert torch.equal(torch.isfinite(o).cpu(), torch.isfinite(ref))
+    assert torch.equal(torch.isnan(lse).cpu(), torch.isnan(rl) | torch.isposinf(rl))
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("where", [3, 120, 149])
+def test_infinite_value_of_a_weight_that_underflows(dtype, dim, where):
+    """A seen key of weight 2^-200 in a tile with hidden keys holds +inf in V: the
+    formula's result is infinite, float32's 0 x infinity NaN; it is never finite."""
+    ctx, n = 150, 40
+    p = Paged(dtype, 1, dim, 16, [ctx], seed=15)
+    p.k[0].zero_()
+    p.k[0][where] = -200.0 / (1.4427 * dim ** 0.5)
+    p.put(p.table[0].cpu().numpy(), p.k[0], p.kc)
+    q = torch.ones((n, 2, dim), device="cuda").to(p.dtype)
+    set_key(p, 0, where, "v", 9, float("inf"))
+    o, _, _ = p.attend(q, [n], 2, 1)
+    sees = torch.arange(ctx - n, ctx, device="cuda") >= where
+    assert not torch.isfinite(o[sees][:, :, 9]).any()
+    o[:, :, 9][sees] = 0
+    assert torch.isfinite(o).all()
