@@ -465,7 +465,11 @@ int dlm_paged_attention_workspace(const dlm_paged_cache *cache, int n_heads, siz
  * A row that sees no key (ctx 0, or mask_block >= 1 and a position below 0)
  * gets zeros and lse -inf; rows of o and lse outside [cu_q[0],
  * cu_q[batch]) are left as they were.  Keys that a row does not see do not reach its
- * result, whatever their K and V hold (infinities and NaN included).
+ * result, whatever their K and V hold (infinities and NaN included), and
+ * neither do other rows' queries.  What a row does see is not hidden: a NaN in
+ * its query or in a seen key gives NaN, an infinite V of a seen key an
+ * infinity or NaN in its column, scores that are all -inf give NaN (0 / 0) and
+ * lse -inf.
  * n_heads is a multiple of n_kv_heads, at most 128 query heads per KV head;
  * batch <= 4096.  q and o are 16-byte aligned, their strides multiples of 16
  * bytes and at least n_heads * head_dim; o does not overlap q, the cache or

@@ -602,7 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (n == 0 && quad == 0 && lane == 0) DLM_TRACE_MARK(6);
           if (whole) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            // (without any key c is 0 and O is not used)
+            const float inv = inverse(l, p.block == 0 || it.pos0 + pos >= 0);
             w0 *= inv;
             w1 *= inv;
           }

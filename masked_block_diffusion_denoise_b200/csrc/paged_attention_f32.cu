@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_f32_kernel(co
         const int pos = div_g(p, r), h = it.g * p.G + r - pos * p.G;
         const int64_t grow = (int64_t)it.row0 + pos;
         const size_t slot = (size_t)blockIdx.x * 2 + it.slot;
-        const float inv = !it.whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
+        const float inv = it.whole ? inverse(l[i], lim[i] > 0) : 1.f;
         float* dst = (float*)p.o + grow * p.o_stride + (int64_t)h * DH;
 #pragma unroll
         for (int j = 0; j < DN / 2; ++j) {

@@ -63,7 +63,7 @@ struct Meta {
   int row0, npos, g, pair;
   int head;            // a partial of an item that started earlier
   int head_ends;       // ... whose last key tile is here
-  int pad;
+  int pos0;            // position of row0
 };
 
 struct Params {
@@ -91,6 +91,9 @@ struct Params {
 __device__ __noinline__ int block_end(int p, int ctx, int block) {
   return (int)min((long long)ctx, ((long long)(p / block) + 1) * block);
 }
+// what a row's sum of products is multiplied by: zeros for a row that sees no key,
+// 0 x infinity for one that does and has only scores of -infinity
+__device__ __forceinline__ float inverse(float l, bool sees) { return sees ? 1.f / l : 0.f; }
 // keys [0, n) that the row at position p sees
 __device__ __forceinline__ int visible(int p, int ctx, int block) {
   if (block == 0) return ctx;
@@ -375,6 +378,7 @@ struct Walker {
         if (it.ts == 0) {
           meta.tail = 1;
           meta.row0 = it.row0;
+          meta.pos0 = it.pos0;
           meta.npos = it.npos;
           meta.g = g;
           meta.pair = it.pair;
@@ -488,7 +492,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const Params p, int n_c
     }
     if (!live) continue;
     const int rp = div_g(p, x), rh = x - rp * p.G, pos = tile * p.npos + rp;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    // (an item that is cut has keys: only a mask can hide them all)
+    const float inv = inverse(l, p.block == 0 || me.pos0 + pos >= 0);
     const int64_t grow = (int64_t)me.row0 + pos;
     const int head = me.g * p.G + rh;
     T* dst = (T*)p.o + grow * p.o_stride + (int64_t)head * DH + col;

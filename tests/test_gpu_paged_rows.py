@@ -197,3 +197,24 @@ def test_infinite_value_of_a_weight_that_underflows(dtype, dim, where):
     assert not torch.isfinite(o[sees][:, :, 9]).any()
     o[:, :, 9][sees] = 0
     assert torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("ctx,n", [(100, 4), (5, 9), (2500, 1), (3000, 200)])
+@pytest.mark.parametrize("block", [0, 1])
+def test_every_score_minus_infinity(dtype, dim, ctx, n, block):
+    """A row that sees keys, all with a score of -inf: 0 / 0, not the zeros of a row that
+    sees none."""
+    p = Paged(dtype, 2, dim, 16, [ctx], seed=16)
+    p.k[0][:, :, 3] = -1
+    p.put(p.table[0].cpu().numpy(), p.k[0], p.kc)
+    q = ready(p, [n], 8, 16)
+    q[::2, 5, 3] = float("inf")
+    o, lse, _ = p.attend(q, [n], 8, block)
+    sees = torch.arange(ctx - n, ctx, device="cuda") >= (0 if block else -n)
+    bad = torch.zeros((n, 8), dtype=torch.bool, device="cuda")
+    bad[::2, 5] = True
+    assert torch.isnan(o[bad & sees[:, None]]).all()
+    assert torch.isfinite(o[~bad & sees[:, None]]).all()
+    assert torch.all(o[~sees] == 0)
+    assert torch.equal(torch.isneginf(lse), bad | ~sees[:, None]) and not torch.isnan(lse).any()
