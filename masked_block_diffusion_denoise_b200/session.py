@@ -200,12 +200,17 @@ class PagedCache:
     """A paged KV cache for a batch of sequences whose lengths differ: pages,
     block tables, free list and lengths as device tensors, and one step's calls
     in order -- resize(), write(), attend().  Nothing reads the lengths back, so
-    a step can be captured into a CUDA graph (its tensors are then reused)."""
+    a step can be captured into a CUDA graph (its tensors are then reused).
+
+    Every call runs on the cache's device, whichever is current."""
 
     def __init__(self, *, n_pages: int, page_size: int, n_heads: int, n_kv_heads: int,
                  head_dim: int, batch: int, max_len: int, max_new: int, dtype: str = "bf16",
                  device="cuda:0"):
-        dev = self.device = torch.device(device)
+        dev = torch.device(device)
+        if dev.index is None:
+            dev = torch.device(dev.type, torch.cuda.current_device())
+        self.device = dev
         self.dtype = _TORCH[dtype]
         self.page_size, self.n_heads, self.batch, self.max_new = page_size, n_heads, batch, max_new
         shape = (n_pages, n_kv_heads, page_size, head_dim)
@@ -230,9 +235,10 @@ class PagedCache:
         if (new_lens.dtype != torch.int32 or new_lens.shape != (self.batch,) or
                 not new_lens.is_contiguous()):
             raise ValueError("resize: new_lens is int32 [batch] without gaps")
-        dlm_paged_resize(self.lens, new_lens, self.lens, self.batch, self.table, self.width,
-                         self.page_size, self.free, self.k.shape[0], self.n_free, self.n_free,
-                         self.cu, self.slots, self.max_new, stream=stream)
+        with torch.cuda.device(self.device):
+            dlm_paged_resize(self.lens, new_lens, self.lens, self.batch, self.table, self.width,
+                             self.page_size, self.free, self.k.shape[0], self.n_free, self.n_free,
+                             self.cu, self.slots, self.max_new, stream=stream)
 
     def write(self, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
         """K and V of the last resize's new tokens, [<= max_new][n_kv_heads][head_dim]
@@ -240,29 +246,35 @@ class PagedCache:
         if k.shape[0] != v.shape[0] or k.shape[0] > self.max_new:
             raise ValueError("write: k and v have one row per new token, at most max_new")
         heads = self.k.shape[1]
-        dlm_paged_kv_write(self.c, k, v, self.slots, k.shape[0], stream=stream,
-                           k_stride=self._stride(k, heads, "k"),
-                           v_stride=self._stride(v, heads, "v"))
+        ks, vs = self._stride(k, heads, "k"), self._stride(v, heads, "v")
+        with torch.cuda.device(self.device):
+            dlm_paged_kv_write(self.c, k, v, self.slots, k.shape[0], k_stride=ks, v_stride=vs,
+                               stream=stream)
 
     def attend(self, q: torch.Tensor, mask_block: int, out: Optional[torch.Tensor] = None,
                lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Attention of the new tokens' queries [rows][n_heads][head_dim] over their
-        sequences; mask_block 0 (every key), 1 (causal) or a block length."""
-        if out is None:
-            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
-        if out.shape != q.shape:
+        sequences; mask_block 0 (every key), 1 (causal) or a block length, the same
+        for the whole batch.  Rows of a sequence that the resize refused hold nothing
+        of use, and rows behind the last sequence are not written."""
+        qs = self._stride(q, self.n_heads, "q")
+        if out is not None and out.shape != q.shape:
             raise ValueError("attend: out has q's shape")
         if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or
                                 not lse.is_contiguous()):
             raise ValueError("attend: lse is float32 [rows][n_heads] without gaps")
-        dlm_paged_attention(self.c, q, out, self.cu, self.lens, self.table, self.width, self.batch,
-                            q.shape[0], self.n_heads, mask_block, self.work, lse=lse,
-                            q_stride=self._stride(q, self.n_heads, "q"),
-                            o_stride=self._stride(out, self.n_heads, "out"), stream=stream)
+        with torch.cuda.device(self.device):
+            if out is None:
+                out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+            dlm_paged_attention(self.c, q, out, self.cu, self.lens, self.table, self.width,
+                                self.batch, q.shape[0], self.n_heads, mask_block, self.work, lse=lse,
+                                q_stride=qs, o_stride=self._stride(out, self.n_heads, "out"), stream=stream)
         return out
 
     def check(self, stream=None) -> None:
-        dlm_paged_check(stream)
+        """Wait for the stream; raises what the device recorded (dlm_paged_check)."""
+        with torch.cuda.device(self.device):
+            dlm_paged_check(stream)
 
     def _stride(self, t: torch.Tensor, heads: int, what: str) -> int:
         """Elements between rows of [rows][heads][head_dim] (0: there is one at most)."""
