@@ -202,7 +202,11 @@ class PagedCache:
     in order -- resize(), write(), attend().  Nothing reads the lengths back, so
     a step can be captured into a CUDA graph (its tensors are then reused).
 
-    Every call runs on the cache's device, whichever is current."""
+    Like a torch operation, every call runs on the cache's device, whichever is
+    current, and on that device's current stream unless `stream` names another (a
+    torch stream or a handle).  With a stream of its own a call does not wait for
+    the current one, and the caller keeps its tensors until it is through; the
+    tensor that attend() makes then belongs to that stream's pool."""
 
     def __init__(self, *, n_pages: int, page_size: int, n_heads: int, n_kv_heads: int,
                  head_dim: int, batch: int, max_len: int, max_new: int, dtype: str = "bf16",
@@ -228,6 +232,8 @@ class PagedCache:
         with torch.cuda.device(dev):
             self.work = torch.empty(dlm_paged_attention_workspace(self.c, n_heads),
                                     dtype=torch.uint8, device=dev)
+            # the first call may come on any stream
+            torch.cuda.current_stream().synchronize()
 
     def resize(self, new_lens: torch.Tensor, stream=None) -> None:
         """Lengths (int32 [batch], device) that the sequences are to have; a
@@ -238,7 +244,7 @@ class PagedCache:
         with torch.cuda.device(self.device):
             dlm_paged_resize(self.lens, new_lens, self.lens, self.batch, self.table, self.width,
                              self.page_size, self.free, self.k.shape[0], self.n_free, self.n_free,
-                             self.cu, self.slots, self.max_new, stream=stream)
+                             self.cu, self.slots, self.max_new, stream=self._stream(stream))
 
     def write(self, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
         """K and V of the last resize's new tokens, [<= max_new][n_kv_heads][head_dim]
@@ -249,7 +255,7 @@ class PagedCache:
         ks, vs = self._stride(k, heads, "k"), self._stride(v, heads, "v")
         with torch.cuda.device(self.device):
             dlm_paged_kv_write(self.c, k, v, self.slots, k.shape[0], k_stride=ks, v_stride=vs,
-                               stream=stream)
+                               stream=self._stream(stream))
 
     def attend(self, q: torch.Tensor, mask_block: int, out: Optional[torch.Tensor] = None,
                lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -264,17 +270,31 @@ class PagedCache:
                                 not lse.is_contiguous()):
             raise ValueError("attend: lse is float32 [rows][n_heads] without gaps")
         with torch.cuda.device(self.device):
+            s = self._stream(stream)
             if out is None:
-                out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+                with torch.cuda.stream(s):
+                    out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
             dlm_paged_attention(self.c, q, out, self.cu, self.lens, self.table, self.width,
                                 self.batch, q.shape[0], self.n_heads, mask_block, self.work, lse=lse,
-                                q_stride=qs, o_stride=self._stride(out, self.n_heads, "out"), stream=stream)
+                                q_stride=qs, o_stride=self._stride(out, self.n_heads, "out"), stream=s)
         return out
 
     def check(self, stream=None) -> None:
         """Wait for the stream; raises what the device recorded (dlm_paged_check)."""
         with torch.cuda.device(self.device):
-            dlm_paged_check(stream)
+            dlm_paged_check(self._stream(stream))
+
+    def _stream(self, stream) -> torch.cuda.Stream:
+        """The stream of a call: the one given, or the device's current one."""
+        if stream is None:
+            return torch.cuda.current_stream(self.device)
+        if isinstance(stream, int):
+            if stream in (0, 1):    # CUDA's names for the default stream
+                return torch.cuda.default_stream(self.device)
+            return torch.cuda.ExternalStream(stream, device=self.device)
+        if stream.device != self.device:
+            raise ValueError("PagedCache: a stream of another device")
+        return stream
 
     def _stride(self, t: torch.Tensor, heads: int, what: str) -> int:
         """Elements between rows of [rows][heads][head_dim] (0: there is one at most)."""

@@ -1,0 +1,128 @@
+"""session.PagedCache on streams: the current one, one that is given, one that
+is being captured."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - collected on CPU-only hosts
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from masked_block_diffusion_denoise_b200.session import PagedCache
+
+HEADS, KV, DIM, B, NEW = 8, 2, 128, 3, 96
+SLEEP = 1 << 27          # cycles: some 70 ms, far beyond a call's time on the host
+
+
+def make(**kw):
+    return PagedCache(n_pages=60, page_size=16, n_heads=HEADS, n_kv_heads=KV, head_dim=DIM, batch=B,
+                      max_len=200, max_new=NEW, **kw)
+
+
+def inputs(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((NEW, HEADS + 2 * KV, DIM), generator=g, device="cuda").to(torch.bfloat16)
+    return x[:, :HEADS], x[:, HEADS:HEADS + KV], x[:, HEADS + KV:]
+
+
+def lens(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def step(pc, want, x, **kw):
+    q, k, v = x
+    pc.resize(want, **kw)
+    pc.write(k, v, **kw)
+    return pc.attend(q, 1, **kw)
+
+
+@pytest.fixture
+def expected():
+    """Results of three steps on the default stream, and their inputs."""
+    pc = make()
+    wants = [[40, 0, 33], [41, 30, 34], [90, 31, 0]]
+    xs = [inputs(s) for s in range(3)]
+    total = [73, 32, 50]
+    return wants, xs, [step(pc, lens(w), x)[:t].clone() for w, x, t in zip(wants, xs, total)], total
+
+
+@pytest.mark.parametrize("built", ["before", "inside"])
+def test_side_stream_is_the_current_one(expected, built):
+    """Inputs that the side stream has yet to write when the calls are made."""
+    wants, xs, outs, total = expected
+    pc = make() if built == "before" else None
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        pc = pc or make()
+        want = lens([0] * B)
+        x = tuple(torch.zeros_like(t) for t in xs[0])
+        for w, src, o, t in zip(wants, xs, outs, total):
+            later = lens(w)
+            torch.cuda._sleep(SLEEP)
+            want.copy_(later)
+            for a, b in zip(x, src):
+                a.copy_(b)
+            got = step(pc, want, x)
+            kept = got[:t].clone()
+            pc.check()
+            assert torch.equal(kept, o)
+
+
+def test_captured_without_naming_the_stream(expected):
+    wants, xs, outs, total = expected
+    pc = make()
+    want, x = lens([0] * B), tuple(torch.zeros_like(t) for t in xs[0])
+    step(pc, want, x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(pc, want, x)
+    for w, src, o, t in zip(wants, xs, outs, total):
+        want.copy_(lens(w))
+        for a, b in zip(x, src):
+            a.copy_(b)
+        graph.replay()
+        pc.check()
+        assert torch.equal(got[:t], o)
+    assert pc.lens.tolist() == wants[-1]
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_stream_given(expected, handle):
+    """The result's memory is the given stream's: what the current stream still does
+    with a freed tensor of the same size does not reach it."""
+    wants, xs, outs, total = expected
+    pc = make()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for w, x, o, t in zip(wants, xs, outs, total):
+        want = lens(w)
+        torch.cuda.synchronize()
+        old = torch.empty_like(xs[0][0])
+        torch.cuda._sleep(SLEEP)
+        old.fill_(7)
+        del old
+        got = step(pc, want, x, stream=s.cuda_stream if handle else s)
+        torch.cuda.synchronize()
+        pc.check(stream=s)
+        assert torch.equal(got[:t], o)
+
+
+def test_two_caches_on_two_streams(expected):
+    wants, xs, outs, total = expected
+    both = [(make(), torch.cuda.Stream()) for _ in range(2)]
+    torch.cuda.synchronize()
+    for w, x, o, t in zip(wants, xs, outs, total):
+        want = lens(w)
+        torch.cuda.synchronize()
+        got = [step(pc, want, x, stream=s) for pc, s in both]
+        torch.cuda.synchronize()
+        for g in got:
+            assert torch.equal(g[:t], o)
+    both[0][0].check()
+
+
+def test_device_without_an_index():
+    assert make(device="cuda").device == torch.device("cuda", torch.cuda.current_device())

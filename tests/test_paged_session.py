@@ -1,4 +1,4 @@
-"""session.PagedCache's device, with fakes in the place of the
+"""session.PagedCache's device and stream, with fakes in the place of the
 library and of torch's guards (no GPU needed)."""
 import contextlib
 
@@ -7,6 +7,11 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from masked_block_diffusion_denoise_b200 import session
+
+
+class Stream:
+    def __init__(self, name, device):
+        self.name, self.device = name, device
 
 
 @pytest.fixture
@@ -21,6 +26,9 @@ def calls(monkeypatch):
         inside.pop()
 
     monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream("current", d or inside[-1]))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda d=None: Stream("default", d))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device: Stream(h, device))
     for name in ("resize", "kv_write", "attention"):
         monkeypatch.setattr(session, "dlm_paged_" + name,
                             lambda *a, stream=None, name=name, **kw: seen.append((name, inside[-1], stream)))
@@ -41,8 +49,24 @@ def step(pc, **kw):
     pc.check(**kw)
 
 
-def test_calls_switch_to_the_cache_s_device(calls):
+def test_calls_switch_to_the_cache_s_device_and_its_current_stream(calls):
     pc, seen = calls
     step(pc)
     assert [name for name, _, _ in seen] == ["resize", "kv_write", "attention", "check"]
-    assert all(dev == pc.device for _, dev, _ in seen)
+    for _, dev, stream in seen:
+        assert dev == pc.device and stream.name == "current" and stream.device == pc.device
+
+
+def test_streams_given(calls):
+    pc, seen = calls
+    mine = Stream("mine", pc.device)
+    step(pc, stream=mine)
+    assert all(s is mine for _, _, s in seen)
+    seen.clear()
+    step(pc, stream=0x7700)
+    assert all(s.name == 0x7700 and s.device == pc.device for _, _, s in seen)
+    seen.clear()
+    step(pc, stream=0)
+    assert all(s.name == "default" for _, _, s in seen)
+    with pytest.raises(ValueError):
+        pc.resize(torch.zeros(2, dtype=torch.int32), stream=Stream("other", torch.device("cuda:0")))
