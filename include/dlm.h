@@ -421,8 +421,11 @@ typedef struct {
  * Order of the stack: the released pages are pushed so that the first
  * (lowest sequence, lowest table column) is on top, then the new pages are
  * popped in order; growing and then shrinking back restores the stack.
- * A stack height outside [0, n_pages], or releases that would pass n_pages,
- * change nothing but the error word (out_lens = cur_lens, slots -1). */
+ * A stack height outside [0, n_pages], releases that would pass n_pages, or a
+ * page id outside [0, n_pages) among those that the call would push, pop or
+ * give slots of, change nothing but the error word (out_lens = cur_lens,
+ * n_free_out = n_free_in, slots -1).  That no page is held twice is for the
+ * caller to keep. */
 int dlm_paged_resize(const int32_t *cur_lens, const int32_t *new_lens, int32_t *out_lens,
                      int batch, int32_t *block_table, int table_width, int page_size,
                      int32_t *free_pages, int n_pages, const int32_t *n_free_in,

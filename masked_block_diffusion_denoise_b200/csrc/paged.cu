@@ -1,6 +1,7 @@
 // The paged KV cache: block tables, free list and slot map from request
 // lengths, and the write of new tokens' K and V into their slots.  (A finished
 // block joins the cache of its sequence: course "Diffusion LLMs", section 14.)
+#include <algorithm>
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -23,15 +24,21 @@ namespace cg = cooperative_groups;
 // k < F_total is released page k and the others come from the free list.
 // Every thread can therefore compute any output by itself, and no output is
 // read back: one launch, one cluster, no order of atomics.  Each CTA of the
-// cluster scans the batch for itself (its sequences' state in shared memory)
-// and then takes its share of the outputs; the cluster barrier between the
-// two allows the outputs to overwrite the inputs.
+// cluster scans the batch for itself (its sequences' state in shared memory),
+// looks at every page id that the call uses, and then takes its share of the
+// outputs; the cluster barrier between the two allows the outputs to overwrite
+// the inputs.
 // Bound by latency (a few hundred KB at most): one sequence that takes two pages
-// 4.5 us a call in a graph, 256 requests of which the last do not get their
-// pages 8.7, 48 prompts of up to 2000 tokens (48 thousand slots) 7.7.
+// 4.8 us a call in a graph, 256 requests of which the last do not get their
+// pages 8.1, 48 prompts of up to 2000 tokens (48 thousand slots) 8.6 (4.5, 8.7 and
+// 7.7 when the ids were not looked at before the outputs).
 // ---------------------------------------------------------------------------
 constexpr int kResizeThreads = 1024;
 constexpr int kResizeSeqs = kPagedMaxBatch;
+// Page ids kept in shared memory; beyond those (pools where a call releases or takes
+// more) an id is looked up again where it is used.  (Looked up again everywhere, by
+// searches in the scan: 10.2 us for the 256 requests, 8.7 for the prompts.)
+constexpr int kResizeIds = 8192;
 constexpr int kRun = 4;   // consecutive slots of a thread: mostly one sequence and page
 
 struct Scan3 {
@@ -63,6 +70,11 @@ __device__ __forceinline__ int find_last(const int* first, int n, int x) {
   return lo;
 }
 
+// four bytes into shared memory, without a register in between
+__device__ __forceinline__ void copy4(int* dst, const int32_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedResize a) {
   extern __shared__ int sm[];
   int* s_cur = sm;               // [B] length now
@@ -70,7 +82,9 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
   int* s_need = s_new + a.B;     // [B] D: new pages before this sequence's
   int* s_gone = s_need + a.B;    // [B] F: released pages before this sequence's
   int* s_tok = s_gone + a.B;     // [B] T: new tokens before this sequence's, capped at max_new
-  int* s_ok = s_tok + a.B;       // [B] served
+  // [B] served sequences: the page they have begun (0 if none); -1 for refused ones
+  int* s_begun = s_tok + a.B;
+  int* s_ids = s_begun + a.B;       // [n_ids] the first popped or released page ids
   __shared__ Scan3 warp_sum[32];
   __shared__ unsigned long long s_taken;   // pages taken
 
@@ -97,10 +111,19 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
     return c;
   };
   Scan3 mine{0, 0, 0};
+  // the page that a growing sequence has begun; of the thread's last one it is loaded
+  // here, so that it comes during the scan
+  auto begun = [&](int b, int cur, int want) {
+    return cur > 0 && want > cur && (cur & page_mask) != 0 && (cur >> sh) < a.W
+               ? a.table[(size_t)b * a.W + (cur >> sh)]
+               : 0;
+  };
+  int begun_last = 0;
   for (int b = b0; b < b1; ++b) {
     const int cur = a.cur[b], want = a.want[b];
     s_cur[b] = cur;
     s_new[b] = want;
+    if (b == b1 - 1) begun_last = begun(b, cur, want);
     mine = mine + change(cur, want);
   }
   auto warp_scan = [&](Scan3 x) {
@@ -127,18 +150,22 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
   // a broken stack: nothing changes
   const bool broken = n_free < 0 || n_free > a.n_pages || n_free + all.gone > a.n_pages;
   const long long have = broken ? 0 : n_free + all.gone;
+  auto valid = [&](int page) { return page >= 0 && page < a.n_pages; };
   long long taken = 0;
+  bool bad = false;   // a page id outside the cache among those that the call uses
   for (int b = b0; b < b1; ++b) {
     const int cur = s_cur[b], want = s_new[b];
     const Scan3 c = change(cur, want);
     const bool fits = cur >= 0 && want >= 0 && pages(want) <= a.W && pages(cur) <= a.W;
     const bool ok = !broken && fits && (c.need == 0 || at.need + c.need <= have) &&
                     (c.tok == 0 || at.tok + c.tok <= a.max_new);
-    s_ok[b] = ok;
     s_need[b] = (int)min(at.need, (long long)INT_MAX);
     s_gone[b] = (int)min(at.gone, (long long)INT_MAX);
     s_tok[b] = (int)min(at.tok, (long long)a.max_new);
     if (ok) taken += c.need;
+    const int page = b == b1 - 1 ? begun_last : begun(b, cur, want);
+    bad |= ok && !valid(page);
+    s_begun[b] = ok ? max(page, 0) : -1;
     at = at + c;
   }
 #pragma unroll
@@ -147,30 +174,50 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
   if (lane == 0 && taken > 0)
     atomicAdd(&s_taken, (unsigned long long)taken);
   __syncthreads();
-  // every CTA has read the lengths and the stack's height
-  if (n_ranks > 1) cg::this_cluster().sync();
-
-  const int F = broken ? 0 : (int)all.gone;
-  const int K = (int)s_taken;
+  int F = broken ? 0 : (int)all.gone;
+  int K = (int)s_taken;
   const int n_tok = (int)min(all.tok, (long long)a.max_new);
-  // page id j of the released ones, and the k-th popped one
-  auto checked = [&](int page) {
-    if (page < 0 || page >= a.n_pages) raise_error(a.err, DLM_EBOUNDS);
-    return page;
+  // Page ids: number k is the k-th popped one, below F also the k-th released one.  All
+  // that the call uses are looked at before any output: one outside the cache would go
+  // on to the stack or to another sequence, so the call changes nothing, as with a
+  // broken stack.  Every CTA copies them to shared memory (the first n_ids), where the
+  // outputs find them: a warp the released ones of its sequences, all copies under way
+  // at once.
+  const int n_ids = min(a.n_pages, kResizeIds), used = max(F, K);
+  auto first_of = [&](int b) { return a.table + (size_t)b * a.W + pages(s_new[b]); };
+  auto lookup = [&](int k) {
+    if (k >= F) return a.free_pages[n_free + F - 1 - k];
+    const int b = find_last(s_gone, a.B, k);
+    return first_of(b)[k - s_gone[b]];
   };
-  auto released = [&](int j) {
-    const int b = find_last(s_gone, a.B, j);
-    return checked(a.table[(size_t)b * a.W + pages(s_new[b]) + (j - s_gone[b])]);
-  };
-  auto popped = [&](int k) {
-    return k < F ? released(k) : checked(a.free_pages[n_free + F - 1 - k]);
-  };
+  for (int b = lane * 32 + warp; F > 0 && b - lane * 32 < a.B; b += kResizeThreads) {
+    const int from = b < a.B ? s_gone[b] : 0;
+    const int n = b < a.B ? (b + 1 < a.B ? s_gone[b + 1] : F) - from : 0;
+    for (uint32_t some = __ballot_sync(0xffffffffu, n > 0); some != 0; some &= some - 1) {
+      const int l = __ffs(some) - 1;
+      const int32_t* src = first_of(__shfl_sync(0xffffffffu, b, l));
+      const int to = __shfl_sync(0xffffffffu, from, l);
+      const int end = min(__shfl_sync(0xffffffffu, n, l), n_ids - to);
+      for (int c = lane; c < end; c += 32) copy4(s_ids + to + c, src + c);
+    }
+  }
+  for (int k = F + tid; k < min(K, n_ids); k += kResizeThreads)
+    copy4(s_ids + k, a.free_pages + (n_free + F - 1 - k));
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  for (int k = tid; k < min(used, n_ids); k += kResizeThreads) bad |= !valid(s_ids[k]);
+  for (int k = n_ids + tid; k < used; k += kResizeThreads) bad |= !valid(lookup(k));
+  auto taken_page = [&](int k) { return k < n_ids ? s_ids[k] : lookup(k); };
+  const bool stop = __syncthreads_or(bad) || broken;
+  if (stop) F = K = 0;
+  // every CTA has read the lengths, the tables and the stack
+  if (n_ranks > 1) cg::this_cluster().sync();
   // outputs, as one list of tasks over the cluster's threads (neighbouring warps'
   // go to different CTAs), so that their chains of loads run side by side
   const int first = (warp * n_ranks + rank) * 32 + lane, step = n_ranks * kResizeThreads;
   if (first == 0) {
-    if (broken) raise_error(a.err, DLM_EBOUNDS);
-    *a.n_free_out = broken ? n_free : n_free + F - K;
+    if (stop) raise_error(a.err, DLM_EBOUNDS);
+    *a.n_free_out = n_free + F - K;
     a.cu[0] = 0;
   }
   const int kept = max(0, F - K);                      // released pages that stay on the stack
@@ -183,8 +230,8 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
       const int t0 = (int)y * kRun;
       int64_t slot[kRun];
       int b = -1, end = t0, col = -1, cur = 0, tb = 0, page_b = 0;
-      bool ok = false;
-      int64_t base = -1;
+      int begun_page = -1;
+      int64_t base = 0;
 #pragma unroll
       for (int u = 0; u < kRun; ++u) {
         const int t = t0 + u;
@@ -193,21 +240,20 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
         if (t >= end) {
           b = find_last(s_tok, a.B, t);
           end = b + 1 < a.B ? s_tok[b + 1] : n_tok;
-          ok = s_ok[b] != 0;
+          begun_page = stop ? -1 : s_begun[b];
           cur = s_cur[b];
           tb = s_tok[b];
           page_b = s_need[b] - pages(cur);
           col = -1;
         }
-        if (!ok) continue;
+        if (begun_page < 0) continue;
         const int pos = cur + (t - tb);
         if (pos >> sh != col) {
           col = pos >> sh;
-          const int page = col < pages(cur) ? checked(a.table[(size_t)b * a.W + col])
-                                            : popped(page_b + col);
-          base = page >= 0 && page < a.n_pages ? (int64_t)page << sh : -1;
+          const int page = col < pages(cur) ? begun_page : taken_page(page_b + col);
+          base = (int64_t)page << sh;
         }
-        if (base >= 0) slot[u] = base + (pos & (int)page_mask);
+        slot[u] = base + (pos & (int)page_mask);
       }
       if (t0 + kRun <= a.max_new && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
         longlong2* dst = reinterpret_cast<longlong2*>(a.slots + t0);
@@ -225,17 +271,17 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const PagedRe
       // a new page into its table (served sequences that need pages are the first
       // of those that need any, so page k's owner is found in D)
       const int k = (int)y, b = find_last(s_need, a.B, k);
-      a.table[(size_t)b * a.W + pages(s_cur[b]) + (k - s_need[b])] = popped(k);
+      a.table[(size_t)b * a.W + pages(s_cur[b]) + (k - s_need[b])] = taken_page(k);
       continue;
     }
     y -= K;
     if (y < kept) {
       // position n_free + y of the stack
-      a.free_pages[n_free + (int)y] = released(F - 1 - (int)y);
+      a.free_pages[n_free + (int)y] = taken_page(F - 1 - (int)y);
       continue;
     }
     const int b = (int)(y - kept);
-    a.out_lens[b] = s_ok[b] ? s_new[b] : s_cur[b];
+    a.out_lens[b] = !stop && s_begun[b] >= 0 ? s_new[b] : s_cur[b];
     a.cu[b + 1] = b + 1 < a.B ? s_tok[b + 1] : n_tok;
   }
 }
@@ -282,12 +328,13 @@ __global__ void __launch_bounds__(kWriteThreads)
 }  // namespace
 
 cudaError_t paged_resize(const PagedResize& a, cudaStream_t st) {
-  const int smem = 6 * a.B * (int)sizeof(int);
-  static_assert(6 * kResizeSeqs * sizeof(int) <= 227 * 1024 - 2048, "batch exceeds shared memory");
+  const int smem = (6 * a.B + std::min(a.n_pages, kResizeIds)) * (int)sizeof(int);
+  constexpr int kMost = (6 * kResizeSeqs + kResizeIds) * (int)sizeof(int);
+  static_assert(kMost <= 227 * 1024 - 2048, "batch exceeds shared memory");
   static DeviceOnce once;
   cudaError_t e = once.get([] {
     return cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                6 * kResizeSeqs * (int)sizeof(int));
+                                kMost);
   });
   if (e != cudaSuccess) return e;
   // One CTA up to a run of slots a thread, then a cluster of up to 8: a CTA more
