@@ -173,13 +173,13 @@ def lib() -> ctypes.CDLL:
 
 def _ptr(x) -> Optional[int]:
     """Device/host address of a torch tensor, an int, or None."""
-    if x is None or x.__class__ is int:
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None or stream.__class__ is int:
+    if stream is None or isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
