@@ -484,8 +484,11 @@ int dlm_paged_attention(const dlm_paged_cache *cache, const void *q, int64_t q_s
                         void *workspace, size_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, then read and clear the current device's error word
- * of the paged calls: DLM_OK, DLM_EBOUNDS or DLM_ETIMEOUT (the text is in
- * dlm_last_error(NULL)). */
+ * of the paged calls, in one step: DLM_OK, DLM_EBOUNDS or DLM_ETIMEOUT (the text
+ * is in dlm_last_error(NULL)).  The word is shared by every caller on the
+ * device: it holds the first error since the last check on any stream, a check
+ * may report what another stream's call recorded, and one check gets it.  Not
+ * while `stream` is captured. */
 int dlm_paged_check(void *stream);
 
 /* Synchronise `stream` and return the device error word (DLM_OK, or

@@ -8,14 +8,20 @@
 
 using namespace dlm;
 
-static __device__ int g_paged_err[1];
+// the error word, and where a check puts what it took from it
+static __device__ int g_paged_err[2];
 
 namespace {
+
+// One step, so that what a kernel of another stream records meanwhile is either
+// taken or stays.
+__global__ void take_error_kernel(int* err) { err[1] = atomicExch(err, 0); }
 
 struct PagedDevice {
   std::once_flag once;
   cudaError_t status = cudaErrorNotReady;
   int* err = nullptr;
+  std::mutex check;   // err[1] is one check's at a time
   int num_sms = 0;
 };
 constexpr int kMaxDevices = 64;
@@ -237,13 +243,20 @@ int dlm_paged_check(void* stream) {
   if (int rc = paged_device(&d, &dev)) return rc;
   if (cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream); e != cudaSuccess)
     return api_cuda_fail("paged_check: cudaStreamSynchronize", e);
+  // in the caller's stream: the legacy stream would wait for work that is not its
   int word = 0;
-  if (cudaError_t e = cudaMemcpy(&word, d->err, sizeof(int), cudaMemcpyDeviceToHost);
-      e != cudaSuccess)
-    return api_cuda_fail("paged_check: read the error word", e);
+  cudaError_t e;
+  {
+    std::lock_guard<std::mutex> one(d->check);
+    take_error_kernel<<<1, 1, 0, (cudaStream_t)stream>>>(d->err);
+    e = cudaGetLastError();
+    if (e == cudaSuccess)
+      e = cudaMemcpyAsync(&word, d->err + 1, sizeof(int), cudaMemcpyDeviceToHost,
+                          (cudaStream_t)stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  }
+  if (e != cudaSuccess) return api_cuda_fail("paged_check: take the error word", e);
   if (word == 0) return DLM_OK;
-  if (cudaError_t e = cudaMemset(d->err, 0, sizeof(int)); e != cudaSuccess)
-    return api_cuda_fail("paged_check: clear the error word", e);
   return api_fail(word, word == DLM_ETIMEOUT ? "paged: device wait timed out"
                                              : "paged: device index check failed");
 }

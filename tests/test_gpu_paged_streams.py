@@ -1,5 +1,7 @@
 """session.PagedCache on streams: the current one, one that is given, one that
 is being captured."""
+import threading
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -9,6 +11,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover - collected on CPU-only hosts
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
+import masked_block_diffusion_denoise_b200 as dlm
 from masked_block_diffusion_denoise_b200.session import PagedCache
 
 HEADS, KV, DIM, B, NEW = 8, 2, 128, 3, 96
@@ -126,3 +129,54 @@ def test_two_caches_on_two_streams(expected):
 
 def test_device_without_an_index():
     assert make(device="cuda").device == torch.device("cuda", torch.cuda.current_device())
+
+
+# ---------------------------------------------------------------------------
+# the error word
+# ---------------------------------------------------------------------------
+
+def bad_write(pc, stream):
+    slots = torch.tensor([1 << 40], device="cuda")
+    row = torch.zeros((1, KV, DIM), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    return lambda: dlm.dlm_paged_kv_write(pc.c, row, row, slots, 1, stream=stream)
+
+
+def test_check_waits_for_its_own_stream_only():
+    pc, s = make(), torch.cuda.Stream()
+    call = bad_write(pc, s)
+    torch.cuda._sleep(1 << 30)       # half a second on the default stream
+    busy = torch.cuda.Event()
+    busy.record()
+    call()
+    with pytest.raises(dlm.DlmError) as e:
+        dlm.dlm_paged_check(s)
+    assert e.value.code == dlm.DLM_EBOUNDS
+    dlm.dlm_paged_check(s)
+    assert not busy.query()
+    torch.cuda.synchronize()
+
+
+def test_one_check_of_two_gets_an_error():
+    pc = make()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    call = bad_write(pc, streams[0])
+    for _ in range(100):
+        call()
+        streams[0].synchronize()
+        start, seen = threading.Barrier(2), []
+
+        def check(s):
+            start.wait()
+            try:
+                dlm.dlm_paged_check(s)
+            except dlm.DlmError as e:
+                seen.append(e.code)
+
+        both = [threading.Thread(target=check, args=(s,)) for s in streams]
+        for t in both:
+            t.start()
+        for t in both:
+            t.join()
+        assert seen == [dlm.DLM_EBOUNDS]
+    dlm.dlm_paged_check()
