@@ -99,8 +99,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_f32_kernel(co
         lim[i] = r < rows ? visible(it.pos0 + div_g(p, r), it.ctx, p.block) : 0;
       }
       __syncthreads();   // the rows before these are done with Q, K, V and P
+      // (rows without keys load nothing: nothing waits for such a copy, and it would
+      // race with the next item's into the same place)
+      const int q_end = it.ts < it.te ? kRows * DH / 4 : 0;
 #pragma unroll 4
-      for (int x = tid; x < kRows * DH / 4; x += kThreads) {
+      for (int x = tid; x < q_end; x += kThreads) {
         const int lr = x / (DH / 4), c = x % (DH / 4) * 4, r = r0 + lr;
         const int pos = div_g(p, r), h = it.g * p.G + r - pos * p.G;
         const bool live = r < rows;

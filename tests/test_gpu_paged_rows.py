@@ -10,7 +10,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU-only ho
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 from oracle import paged as OP
-from test_gpu_paged import Paged, ready
+from test_gpu_paged import Paged, check, ready
 
 # Sequences of several key tiles a CTA: a row's softmax reference has earlier
 # tiles to fall behind.  (heads, kv heads): G 4; 3, 5 and 7 do not divide a
@@ -218,3 +218,27 @@ def test_every_score_minus_infinity(dtype, dim, ctx, n, block):
     assert torch.isfinite(o[~bad & sees[:, None]]).all()
     assert torch.all(o[~sees] == 0)
     assert torch.equal(torch.isneginf(lse), bad | ~sees[:, None]) and not torch.isnan(lse).any()
+
+
+@pytest.mark.parametrize("dtype,dim,heads,kv", [("f32", 64, 4, 4), ("f32", 128, 8, 1), ("f32", 32, 100, 1),
+                                                ("bf16", 128, 8, 2)])
+@pytest.mark.parametrize("block", [0, 1])
+def test_rows_without_keys_between_rows_with_keys(dtype, dim, heads, kv, block):
+    """Items without any key directly before items with keys, many for each CTA: the bits
+    of the same sequences by themselves."""
+    ctx = [0 if b % 3 else 5 + b % 11 for b in range(600)]
+    new = [2 if c == 0 else 1 for c in ctx]
+    p = Paged(dtype, kv, dim, 8, ctx, seed=17)
+    q = ready(p, new, heads, 17)
+    o, lse, cu = p.attend(q, new, heads, block)
+    # queries of the rows without keys, which are loaded nowhere, are NaN
+    loud = q.clone()
+    for b, c in enumerate(ctx):
+        if c == 0:
+            loud[cu[b]:cu[b + 1]] = float("nan")
+    for _ in range(5):
+        o2, lse2, _ = p.attend(loud, new, heads, block)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    full = torch.tensor([c > 0 for c, n in zip(ctx, new) for _ in range(n)], device="cuda")
+    assert torch.all(o[~full] == 0) and torch.isneginf(lse[~full]).all()
+    check(p, q, o, lse, cu, new, heads, block)
