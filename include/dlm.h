@@ -435,8 +435,9 @@ int dlm_paged_resize(const int32_t *cur_lens, const int32_t *new_lens, int32_t *
 /* Write n_tokens rows of K and V into the cache: row t ([n_kv_heads]
  * [head_dim], rows k_stride / v_stride elements apart, already rotated, in
  * the cache's type) goes to slots[t].  A negative slot is skipped (padding).
- * Two rows with the same slot leave one of the two (which one is not
- * defined).  k and v are 16-byte aligned and the strides multiples of 16
+ * The others are distinct, as dlm_paged_resize makes them: what a slot holds
+ * that two rows were written to is not defined (a mixture of both rows, K and V
+ * each by itself), other slots hold their rows.  k and v are 16-byte aligned and the strides multiples of 16
  * bytes and at least n_kv_heads * head_dim; k and v do not overlap the
  * cache. */
 int dlm_paged_kv_write(const dlm_paged_cache *cache, const void *k, const void *v,

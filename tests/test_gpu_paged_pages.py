@@ -120,3 +120,35 @@ def test_more_pages_than_a_block_keeps(case):
     else:
         dlm.dlm_paged_check()
         same_resize(got, OP.resize(cur, new, table, page, free, 200000))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_that_share_a_slot_leave_the_others_alone(dtype):
+    """Slots that several rows name hold pieces of those rows; the others their row, and
+    what no row names stays."""
+    kv, dim, page, n_pages, n = 3, 64, 16, 60, 500
+    kc, vc = (torch.full((n_pages, kv, page, dim), -1.0, dtype=dtype, device="cuda") for _ in range(2))
+    k = torch.arange(n, device="cuda").to(dtype)[:, None, None].expand(n, kv, dim).contiguous()
+    v = (k + 1).contiguous() if dtype == torch.float32 else k.clone()
+    slots = torch.arange(n, device="cuda") + 7
+    slots[100:200] = 64           # a hundred rows, one slot
+    slots[300:310] = slots[490:500]
+    c = dlm.dlm_paged_cache(kc.data_ptr(), vc.data_ptr(), n_pages, page, kv, dim,
+                            dlm.DLM_F32 if dtype == torch.float32 else dlm.DLM_BF16)
+    dlm.dlm_paged_kv_write(c, k, v, slots, n)
+    dlm.dlm_paged_check()
+    named = {}
+    for row, s in enumerate(slots.tolist()):
+        named.setdefault(s, []).append(row)
+    for cache, src in ((kc, k), (vc, v)):
+        got = cache.permute(0, 2, 1, 3).reshape(n_pages * page, kv * dim).double().cpu()
+        want = src[:, 0, 0].double().cpu()
+        per = 16 // cache.element_size()
+        for s in range(n_pages * page):
+            rows = named.get(s)
+            if rows is None:
+                assert torch.all(got[s] == -1)
+            else:
+                pieces = got[s].reshape(-1, per)
+                assert torch.all(pieces == pieces[:, :1])
+                assert all(x in want[rows] for x in pieces[:, 0])
