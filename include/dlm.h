@@ -438,8 +438,8 @@ int dlm_paged_resize(const int32_t *cur_lens, const int32_t *new_lens, int32_t *
  * The others are distinct, as dlm_paged_resize makes them: what a slot holds
  * that two rows were written to is not defined (a mixture of both rows, K and V
  * each by itself), other slots hold their rows.  k and v are 16-byte aligned and the strides multiples of 16
- * bytes and at least n_kv_heads * head_dim; k and v do not overlap the
- * cache. */
+ * bytes, at least n_kv_heads * head_dim and below 2^40 bytes; k and v do not
+ * overlap the cache. */
 int dlm_paged_kv_write(const dlm_paged_cache *cache, const void *k, const void *v,
                        int64_t k_stride, int64_t v_stride, const int64_t *slots, int n_tokens,
                        void *stream);
@@ -476,8 +476,8 @@ int dlm_paged_attention_workspace(const dlm_paged_cache *cache, int n_heads, siz
  * lse -inf.
  * n_heads is a multiple of n_kv_heads, at most 128 query heads per KV head;
  * batch <= 4096.  q and o are 16-byte aligned, their strides multiples of 16
- * bytes and at least n_heads * head_dim; o does not overlap q, the cache or
- * the workspace.  `workspace` is 256-byte aligned. */
+ * bytes, at least n_heads * head_dim and below 2^40 bytes; o does not overlap q,
+ * the cache or the workspace.  `workspace` is 256-byte aligned. */
 int dlm_paged_attention(const dlm_paged_cache *cache, const void *q, int64_t q_stride, void *o,
                         int64_t o_stride, float *lse, const int32_t *cu_q,
                         const int32_t *ctx_lens, const int32_t *block_table, int table_width,

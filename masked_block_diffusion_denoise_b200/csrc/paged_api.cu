@@ -100,11 +100,12 @@ PagedKV kv_of(const dlm_paged_cache* c) {
                  c->dtype == DLM_BF16 ? 2 : 4};
 }
 
-// rows of `width` elements, `stride` apart: 16-byte pieces, no overlap
+// rows of `width` elements, `stride` apart: 16-byte pieces, no overlap, and a
+// stride that a tensor map can hold (below 2^40 bytes)
 const char* rows_problem(const void* p, int64_t stride, int64_t width, int esize) {
   if (!aligned(p, 16)) return "paged: rows are not 16-byte aligned";
-  if (stride < width || stride * esize % 16 != 0 || stride > (1ll << 40))
-    return "paged: a row stride must be a multiple of 16 bytes and at least the row";
+  if (stride < width || stride >= (1ll << 40) / esize || stride * esize % 16 != 0)
+    return "paged: a row stride must be a multiple of 16 bytes, at least the row and below 2^40 bytes";
   return nullptr;
 }
 

@@ -40,3 +40,29 @@ def test_a_call_with_an_address_of_a_subclass():
     with pytest.raises(dlm.DlmError):
         dlm.dlm_paged_resize(Handle(64), Handle(64), Handle(64), 0, Handle(64), 1, 8, Handle(64), 1,
                              Handle(64), Handle(64), Handle(64), None, 0, stream=Name.LEGACY)
+
+
+@pytest.mark.parametrize("dtype,stride", [(dlm.DLM_BF16, 2 ** 39), (dlm.DLM_BF16, 2 ** 40),
+                                          (dlm.DLM_F32, 2 ** 38), (dlm.DLM_BF16, 2 ** 62)])
+def test_strides_beyond_a_tensor_map_are_refused(dtype, stride):
+    """As bad arguments, before anything is asked of the device."""
+    a = 0x10000
+
+    class Work:
+        def numel(self):
+            return 1 << 30
+
+        def element_size(self):
+            return 1
+
+        def data_ptr(self):
+            return a
+
+    c = dlm.dlm_paged_cache(a, a, 16, 16, 2, 128, dtype)
+    for fn, args, kw in ((dlm.dlm_paged_kv_write, (c, a, a, a, 4), ("k_stride", "v_stride")),
+                         (dlm.dlm_paged_attention, (c, a, a, a, a, a, 8, 1, 4, 4, 1, Work()),
+                          ("q_stride", "o_stride"))):
+        for name in kw:
+            with pytest.raises(dlm.DlmError) as e:
+                fn(*args, **{name: stride})
+            assert e.value.code == dlm.DLM_EINVAL, name
