@@ -488,8 +488,8 @@ int dlm_paged_attention(const dlm_paged_cache *cache, const void *q, int64_t q_s
  * of the paged calls, in one step: DLM_OK, DLM_EBOUNDS or DLM_ETIMEOUT (the text
  * is in dlm_last_error(NULL)).  The word is shared by every caller on the
  * device: it holds the first error since the last check on any stream, a check
- * may report what another stream's call recorded, and one check gets it.  Not
- * while `stream` is captured. */
+ * may report what another stream's call recorded, and one check gets it.
+ * DLM_EINVAL for a stream that is being captured (the capture goes on). */
 int dlm_paged_check(void *stream);
 
 /* Synchronise `stream` and return the device error word (DLM_OK, or

@@ -13,6 +13,12 @@ static __device__ int g_paged_err[2];
 
 namespace {
 
+// A CUDA error is returned, and not left behind for the caller's next CUDA call to find.
+int cuda_problem(const char* where, cudaError_t e) {
+  cudaGetLastError();
+  return api_cuda_fail(where, e);
+}
+
 // One step, so that what a kernel of another stream records meanwhile is either
 // taken or stays.
 __global__ void take_error_kernel(int* err) { err[1] = atomicExch(err, 0); }
@@ -30,10 +36,8 @@ PagedDevice g_paged[kMaxDevices];
 // the current device's state in *out, looked up on first use; a DLM status
 int paged_device(PagedDevice** out, int* device = nullptr) {
   int dev = 0;
-  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) {
-    cudaGetLastError();
-    return api_cuda_fail("paged: cudaGetDevice", e);
-  }
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess)
+    return cuda_problem("paged: cudaGetDevice", e);
   if (dev < 0 || dev >= kMaxDevices) return api_fail(DLM_EINVAL, "paged: device index out of range");
   PagedDevice& d = g_paged[dev];
   std::call_once(d.once, [&d, dev] {
@@ -43,7 +47,7 @@ int paged_device(PagedDevice** out, int* device = nullptr) {
     if (d.status == cudaSuccess)
       d.status = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
   });
-  if (d.status != cudaSuccess) return api_cuda_fail("paged: device set-up", d.status);
+  if (d.status != cudaSuccess) return cuda_problem("paged: device set-up", d.status);
   *out = &d;
   if (device != nullptr) *device = dev;
   return DLM_OK;
@@ -144,7 +148,7 @@ int dlm_paged_resize(const int32_t* cur_lens, const int32_t* new_lens, int32_t* 
                       page_shift(page_size), free_pages, n_pages, n_free_in, n_free_out, cu_new,
                       slots, max_new, d->err};
   if (cudaError_t e = paged_resize(a, (cudaStream_t)stream); e != cudaSuccess)
-    return api_cuda_fail("paged_resize launch", e);
+    return cuda_problem("paged_resize launch", e);
   return DLM_OK;
 }
 
@@ -171,7 +175,7 @@ int dlm_paged_kv_write(const dlm_paged_cache* cache, const void* k, const void* 
       return api_fail(DLM_EINVAL, "paged_kv_write: a pointer is not memory of the current device");
   cudaError_t e =
       paged_kv_write(c, k, v, k_stride, v_stride, slots, n_tokens, d->err, (cudaStream_t)stream);
-  if (e != cudaSuccess) return api_cuda_fail("paged_kv_write launch", e);
+  if (e != cudaSuccess) return cuda_problem("paged_kv_write launch", e);
   return DLM_OK;
 }
 
@@ -233,7 +237,7 @@ int dlm_paged_attention(const dlm_paged_cache* cache, const void* q, int64_t q_s
   cudaError_t e = c.esize == 2 ? paged_attention_tc(a, d->num_sms, st)
                                 : paged_attention_f32(a, d->num_sms, st);
   if (e != cudaSuccess)
-    return api_cuda_fail("paged_attention launch", e);
+    return cuda_problem("paged_attention launch", e);
   return DLM_OK;
 }
 
@@ -242,8 +246,14 @@ int dlm_paged_check(void* stream) {
   PagedDevice* d = nullptr;
   int dev = 0;
   if (int rc = paged_device(&d, &dev)) return rc;
+  // (to wait for a stream that is being captured would end the capture)
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaError_t e = cudaStreamIsCapturing((cudaStream_t)stream, &capture); e != cudaSuccess)
+    return cuda_problem("paged_check: cudaStreamIsCapturing", e);
+  if (capture != cudaStreamCaptureStatusNone)
+    return api_fail(DLM_EINVAL, "paged_check: the stream is being captured");
   if (cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream); e != cudaSuccess)
-    return api_cuda_fail("paged_check: cudaStreamSynchronize", e);
+    return cuda_problem("paged_check: cudaStreamSynchronize", e);
   // in the caller's stream: the legacy stream would wait for work that is not its
   int word = 0;
   cudaError_t e;
@@ -256,7 +266,7 @@ int dlm_paged_check(void* stream) {
                           (cudaStream_t)stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
   }
-  if (e != cudaSuccess) return api_cuda_fail("paged_check: take the error word", e);
+  if (e != cudaSuccess) return cuda_problem("paged_check: take the error word", e);
   if (word == 0) return DLM_OK;
   return api_fail(word, word == DLM_ETIMEOUT ? "paged: device wait timed out"
                                              : "paged: device index check failed");

@@ -180,3 +180,19 @@ def test_one_check_of_two_gets_an_error():
             t.join()
         assert seen == [dlm.DLM_EBOUNDS]
     dlm.dlm_paged_check()
+
+
+def test_check_refuses_a_captured_stream_and_lets_the_capture_go_on(expected):
+    wants, xs, outs, total = expected
+    pc = make()
+    want = lens(wants[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(dlm.DlmError) as e:
+            pc.check()
+        got = step(pc, want, xs[0])
+    assert e.value.code == dlm.DLM_EINVAL
+    graph.replay()
+    pc.check()
+    assert torch.equal(got[:total[0]], outs[0])
