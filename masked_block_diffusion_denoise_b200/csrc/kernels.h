@@ -5,8 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
-
+#include "device_once.h"
 #include "lm_epilogue.cuh"
 
 namespace dlm {
@@ -207,21 +206,6 @@ cudaError_t commit_step(const SelectArgs& a, int32_t* tokens, uint8_t* committed
                         uint8_t* done, int32_t* eos_pos, int32_t* prev_cand, int32_t* stable,
                         const float* part, int n_part, int32_t* cand, float* conf, float* ent,
                         dlm_canvas_stats* stats, const int* n_active, int* err, cudaStream_t st);
-
-// A result computed once per device (function attributes are per device)
-constexpr int kMaxDeviceOnce = 64;
-struct DeviceOnce {
-  std::once_flag flag[kMaxDeviceOnce];
-  cudaError_t result[kMaxDeviceOnce];
-  template <typename F>
-  cudaError_t get(F&& f) {
-    int dev = 0;
-    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDeviceOnce) return cudaErrorInvalidDevice;
-    std::call_once(flag[dev], [&] { result[dev] = f(); });
-    return result[dev];
-  }
-};
 
 // ---- paged.cu: the paged KV cache ---------------------------------------------
 constexpr int kPagedMaxBatch = 4096;   // sequences of a paged call (their scan state is in shared memory)

@@ -24,30 +24,28 @@ int cuda_problem(const char* where, cudaError_t e) {
 __global__ void take_error_kernel(int* err) { err[1] = atomicExch(err, 0); }
 
 struct PagedDevice {
-  std::once_flag once;
-  cudaError_t status = cudaErrorNotReady;
   int* err = nullptr;
   std::mutex check;   // err[1] is one check's at a time
   int num_sms = 0;
 };
-constexpr int kMaxDevices = 64;
-PagedDevice g_paged[kMaxDevices];
+PagedDevice g_paged[kMaxDeviceOnce];
+DeviceOnce g_paged_once;
 
 // the current device's state in *out, looked up on first use; a DLM status
 int paged_device(PagedDevice** out, int* device = nullptr) {
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess)
     return cuda_problem("paged: cudaGetDevice", e);
-  if (dev < 0 || dev >= kMaxDevices) return api_fail(DLM_EINVAL, "paged: device index out of range");
+  if (dev < 0 || dev >= kMaxDeviceOnce) return api_fail(DLM_EINVAL, "paged: device index out of range");
   PagedDevice& d = g_paged[dev];
-  std::call_once(d.once, [&d, dev] {
+  const cudaError_t e = g_paged_once.get([&d, dev] {
     void* p = nullptr;
-    d.status = cudaGetSymbolAddress(&p, g_paged_err);
+    const cudaError_t status = cudaGetSymbolAddress(&p, g_paged_err);
+    if (status != cudaSuccess) return status;
     d.err = static_cast<int*>(p);
-    if (d.status == cudaSuccess)
-      d.status = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
+    return cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
   });
-  if (d.status != cudaSuccess) return cuda_problem("paged: device set-up", d.status);
+  if (e != cudaSuccess) return cuda_problem("paged: device set-up", e);
   *out = &d;
   if (device != nullptr) *device = dev;
   return DLM_OK;
