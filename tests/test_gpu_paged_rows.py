@@ -9,8 +9,9 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover - collected on CPU-only hosts
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
+import masked_block_diffusion_denoise_b200 as dlm
 from oracle import paged as OP
-from test_gpu_paged import Paged, check, ready
+from test_gpu_paged import DT, Paged, check, ready
 
 # Sequences of several key tiles a CTA: a row's softmax reference has earlier
 # tiles to fall behind.  (heads, kv heads): G 4; 3, 5 and 7 do not divide a
@@ -242,3 +243,70 @@ def test_rows_without_keys_between_rows_with_keys(dtype, dim, heads, kv, block):
     full = torch.tensor([c > 0 for c, n in zip(ctx, new) for _ in range(n)], device="cuda")
     assert torch.all(o[~full] == 0) and torch.isneginf(lse[~full]).all()
     check(p, q, o, lse, cu, new, heads, block)
+
+
+# ---------------------------------------------------------------------------
+# the far ends of what the calls allow
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+def test_blocks_as_long_as_an_int(dtype, dim):
+    """One block holds every position: all keys for rows from position 0 on."""
+    p = Paged(dtype, 2, dim, 16, [300, 5, 0], seed=18)
+    new = [40, 9, 2]
+    q = ready(p, new, 8, 18)
+    o, lse, cu = p.attend(q, new, 8, 2 ** 31 - 1)
+    check(p, q, o, lse, cu, new, 8, 2 ** 31 - 1)
+    o0, lse0, _ = p.attend(q, new, 8, 300)
+    assert torch.equal(o, o0) and torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("scale", [1e-45, 1e-30, 1e3])
+def test_scales(dtype, dim, scale):
+    """The smallest scale makes the mean of the values, a large one picks the largest score."""
+    p = Paged(dtype, 2, dim, 16, [500, 3], seed=19)
+    q = ready(p, [3, 1], 4, 19)
+    o, lse, cu = p.attend(q, [3, 1], 4, 0, scale=scale)
+    check(p, q, o, None, cu, [3, 1], 4, 0, scale=scale)
+    if scale < 1:
+        # all scores 0: log of the number of keys, a sum of that many ones in float32
+        want = torch.log(torch.tensor([500.0, 500, 500, 3], device="cuda", dtype=torch.float64))
+        assert bool(((lse.double() - want[:, None]).abs() <= 500 * 2.0 ** -23 + 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS[:3])
+def test_sequences_that_share_pages(dtype, dim):
+    """A common prefix in the same pages, tails of their own: as if each had a copy."""
+    page, prefix, ctx = 16, 640, [700, 655, 641, 900]
+    p = Paged(dtype, 2, dim, page, ctx, seed=20)
+    for b in range(1, 4):
+        p.table[b, :prefix // page] = p.table[0, :prefix // page]
+        p.k[b][:prefix], p.v[b][:prefix] = p.k[0][:prefix], p.v[0][:prefix]
+    new = [20, 1, 1, 130]
+    q = ready(p, new, 8, 20)
+    o, lse, cu = p.attend(q, new, 8, 1)
+    check(p, q, o, lse, cu, new, 8, 1)
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_cache_beyond_32_bit_offsets(dtype, dim):
+    """Pages at both ends of a cache of more than 2^32 elements, written and read: the bits of
+    a small cache.  (A hidden infinite V, which is looked up in the pages again.)"""
+    t, code = DT[dtype]
+    kv, page, heads, n, ctx = 2, 256, 8, 40, 600
+    n_pages = 2 ** 32 // (kv * page * dim) + 50
+    small = Paged(dtype, kv, dim, page, [ctx], seed=21, junk=0.0)
+    set_key(small, 0, ctx - 3, "v", 1, float("inf"))
+    q = ready(small, [n], heads, 21)
+    o, lse, _ = small.attend(q, [n], heads, 1)
+    kc, vc = (torch.empty((n_pages, kv, page, dim), dtype=t, device="cuda") for _ in range(2))
+    ids = torch.tensor([n_pages - 1, 0, n_pages - 2], device="cuda")
+    kc[ids], vc[ids] = 0, 0
+    at = torch.arange(ctx, device="cuda")
+    c = dlm.dlm_paged_cache(kc.data_ptr(), vc.data_ptr(), n_pages, page, kv, dim, code)
+    dlm.dlm_paged_kv_write(c, small.k[0], small.v[0], ids[at // page] * page + at % page, ctx)
+    small.cache, small.table = c, ids.int()[None].contiguous()
+    o2, lse2, _ = small.attend(q, [n], heads, 1)
+    assert torch.isinf(o[-3:, :, 1]).all() and torch.isfinite(o[:-3]).all()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
