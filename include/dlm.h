@@ -458,7 +458,7 @@ int dlm_paged_attention_workspace(const dlm_paged_cache *cache, int n_heads, siz
  *   cu_q     int32 [batch+1], ascending from >= 0 to <= n_tokens
  *   ctx_lens int32 [batch]: length of sequence b, its chunk included: row i of
  *            a chunk of n is position ctx - n + i
- *   mask_block  0: every row sees all of [0, ctx) (a canvas being denoised);
+ *   mask_block  of the whole batch.  0: every row sees all of [0, ctx) (a canvas being denoised);
  *            1: causal; c > 1: causal between blocks of c positions (the
  *            clean pass over finished blocks): the row at position p sees
  *            keys below min(ctx, (p / c + 1) * c)
@@ -473,7 +473,10 @@ int dlm_paged_attention_workspace(const dlm_paged_cache *cache, int n_heads, siz
  * neither do other rows' queries.  What a row does see is not hidden: a NaN in
  * its query or in a seen key gives NaN, an infinite V of a seen key an
  * infinity or NaN in its column, scores that are all -inf give NaN (0 / 0) and
- * lse -inf.
+ * lse -inf.  Sums and softmax statistics are float32; DLM_BF16 rounds each
+ * probability to bf16 before its product with V.  The same call repeats its
+ * bits; with other lengths beside it a sequence's work may be cut elsewhere and
+ * its sums be added in another order.
  * n_heads is a multiple of n_kv_heads, at most 128 query heads per KV head;
  * batch <= 4096.  q and o are 16-byte aligned, their strides multiples of 16
  * bytes, at least n_heads * head_dim and below 2^40 bytes; o does not overlap q,

@@ -19,21 +19,28 @@
 // tile in shared memory is [16 groups of 8 rows][half][8 rows][128 bytes], with
 // one stride between 8-row groups, which is what the MMA descriptors need.
 //
-// What bounds it (32 query / 8 KV heads x 128 unless said otherwise):
-//   single tokens of 61 sequences over 1024..4096 keys: HBM, 655 MB in 119 us, 5.5
-//   TB/s; range, first pages and first tile take 7 us of it;
-//   canvases of 32 over 32768 keys: HBM, 540 MB in 104 us, 5.2 TB/s;
-//   chunks of up to 4096 over up to 8192 keys, causal: the softmax, 1.33 TFLOP in 1262
-//   us, 1.06 PFLOP/s (1.45 ms where calls follow each other and the power limit
-//   lowers the clock).  A pair of 128 x 128 tiles takes 3900 cycles, 1025 of them
+// What bounds it (32 query / 8 KV heads x 128 unless said otherwise; a call from
+// Python, and in a graph of ten):
+//   single tokens of 61 sequences over 1024..4096 keys: HBM, 655 MB in 138 us, 4.7
+//   TB/s (120 us, 5.5); range, first pages and first tile take 7 us of it;
+//   canvases of 32 over 32768 keys: HBM, 540 MB in 122 us, 4.4 TB/s (104 us, 5.2);
+//   chunks of up to 4096 over up to 8192 keys, causal: the softmax, 1.33 TFLOP in 1526
+//   us, 0.87 PFLOP/s (1317 to 1457), where calls follow each other and the power limit
+//   lowers the clock (1262 was the best seen; variants are compared with that).  A pair of 128 x 128 tiles takes 3900 cycles, 1025 of them
 //   tensor work and 2090 the exponential unit's: a warp by itself needs 1950 for its
 //   128 exponentials a lane, with their loads from and stores to tensor memory (the
 //   unit alone 1050), and the two warps of a scheduler side by side need no less
 //   than in turns;
 //   finished blocks of 256, 16 / 4 heads x 64, 700..1800 new tokens of 3 sequences: the
-//   same, 31.6 GFLOP in 73 us, 11 of them before the first P;
-//   a canvas of 32 over 2048 keys: latency, 16.5 us: range 2.6, its item and page ids 1.6,
-//   first tile 0.9, first P 1.9, results 1.3, their stores and the join.
+//   same, 31.6 GFLOP in 79 us (78), 11 of them before the first P;
+//   a canvas of 32 over 2048 keys: latency, 16.8 us (16.7): range 2.6, its item and page ids
+//   1.6, first tile 0.9, first P 1.9, results 1.3; the rest is the stores of its partials
+//   and the join.
+//
+// Precision: scores, softmax statistics and O are float32; each probability is rounded
+// to bf16, the tensor core's operand type, before P V and summed unrounded.  Outputs are
+// 0.0020 to 0.0023 off the 64-bit result (2-norm, relative), 0.0017 of it the rounding
+// of the result itself.
 #include "paged_attn.cuh"
 
 namespace dlm {

@@ -10,8 +10,13 @@
 // arithmetic.  Work is cut into equal ranges over all CTAs and joined as in the
 // bf16 kernel, so that a few short sequences still spread over the GPU.
 //
-// Bound by latency at the float32 model's sizes (4 heads x 64, 9 chunks of up to 96
-// tokens over up to 500 keys, causal, 0.12 GFLOP: 22.6 us a call with the join).  At
+// All 64 rows are computed, however few hold a query, and every K and V element is
+// multiplied with each: 32 FLOP a byte, which caps items of few rows at 1 TB/s (single
+// tokens of 61 sequences over 1024..4096 keys, 4 KV heads x 64: 318 us, 1.03 TB/s, with
+// 1 and with 4 query heads a KV head; bytes alone 50 us).
+//
+// Bound by latency for chunks of the float32 model's sizes (4 heads x 64, 9 chunks of up to
+// 96 tokens over up to 500 keys, causal, 0.12 GFLOP: 22.9 us a call with the join).  At
 // larger ones (700..2000 tokens over up to 4000 keys) it reaches 32 TFLOP/s: eight
 // 16-byte loads from shared memory for 64 FMAs a thread.
 #include "paged_attn.cuh"
