@@ -6,6 +6,7 @@ kernels through the functions of this package.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 from typing import Dict, Optional
 
@@ -19,6 +20,7 @@ from . import (DLM_BF16, DLM_F32, DLM_MASK, DLM_UNIFORM, dlm_canvas, dlm_canvas_
                dlm_paged_attention_workspace, dlm_paged_cache, dlm_paged_check,
                dlm_paged_kv_write, dlm_paged_resize, dlm_sampler_params, dlm_weights)
 
+_NOTHING = contextlib.nullcontext()
 _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
 _NP_TYPESTR = {torch.float32: "<f4", torch.bfloat16: "<u2", torch.int32: "<i4",
                torch.uint8: "|u1"}
@@ -233,7 +235,8 @@ class PagedCache:
             self.work = torch.empty(dlm_paged_attention_workspace(self.c, n_heads),
                                     dtype=torch.uint8, device=dev)
             # the first call may come on any stream
-            torch.cuda.current_stream().synchronize()
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     def resize(self, new_lens: torch.Tensor, stream=None) -> None:
         """Lengths (int32 [batch], device) that the sequences are to have; a
@@ -241,7 +244,7 @@ class PagedCache:
         if (new_lens.dtype != torch.int32 or new_lens.shape != (self.batch,) or
                 not new_lens.is_contiguous()):
             raise ValueError("resize: new_lens is int32 [batch] without gaps")
-        with torch.cuda.device(self.device):
+        with self._on_device():
             dlm_paged_resize(self.lens, new_lens, self.lens, self.batch, self.table, self.width,
                              self.page_size, self.free, self.k.shape[0], self.n_free, self.n_free,
                              self.cu, self.slots, self.max_new, stream=self._stream(stream))
@@ -253,7 +256,7 @@ class PagedCache:
             raise ValueError("write: k and v have one row per new token, at most max_new")
         heads = self.k.shape[1]
         ks, vs = self._stride(k, heads, "k"), self._stride(v, heads, "v")
-        with torch.cuda.device(self.device):
+        with self._on_device():
             dlm_paged_kv_write(self.c, k, v, self.slots, k.shape[0], k_stride=ks, v_stride=vs,
                                stream=self._stream(stream))
 
@@ -269,10 +272,14 @@ class PagedCache:
         if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or
                                 not lse.is_contiguous()):
             raise ValueError("attend: lse is float32 [rows][n_heads] without gaps")
-        with torch.cuda.device(self.device):
+        with self._on_device():
             s = self._stream(stream)
-            if out is None:
-                with torch.cuda.stream(s):
+            if out is None and stream is None:
+                out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+            elif out is None:
+                pool = s if isinstance(s, torch.cuda.Stream) else \
+                    torch.cuda.ExternalStream(s.cuda_stream, device=self.device)
+                with torch.cuda.stream(pool):
                     out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
             dlm_paged_attention(self.c, q, out, self.cu, self.lens, self.table, self.width,
                                 self.batch, q.shape[0], self.n_heads, mask_block, self.work, lse=lse,
@@ -281,18 +288,25 @@ class PagedCache:
 
     def check(self, stream=None) -> None:
         """Wait for the stream; raises what the device recorded (dlm_paged_check)."""
-        with torch.cuda.device(self.device):
+        with self._on_device():
             dlm_paged_check(self._stream(stream))
 
-    def _stream(self, stream) -> torch.cuda.Stream:
-        """The stream of a call: the one given, or the device's current one."""
+    def _on_device(self):
+        """The cache's device as the current one (a guard takes microseconds: only where needed)."""
+        if torch.cuda.current_device() == self.device.index:
+            return _NOTHING
+        return torch.cuda.device(self.device)
+
+    def _stream(self, stream):
+        """The stream of a call: the one given, or the device's current one (its handle: a
+        stream object of torch's takes microseconds to make)."""
         if stream is None:
-            return torch.cuda.current_stream(self.device)
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
         if isinstance(stream, int):
             if stream in (0, 1):    # CUDA's names for the default stream
                 return torch.cuda.default_stream(self.device)
             return torch.cuda.ExternalStream(stream, device=self.device)
-        if stream.device != self.device:
+        if getattr(stream, "device", self.device) != self.device:
             raise ValueError("PagedCache: a stream of another device")
         return stream
 

@@ -196,3 +196,34 @@ def test_check_refuses_a_captured_stream_and_lets_the_capture_go_on(expected):
     graph.replay()
     pc.check()
     assert torch.equal(got[:total[0]], outs[0])
+
+
+def test_any_object_with_a_stream_handle(expected):
+    wants, xs, outs, total = expected
+
+    class Handle:
+        def __init__(self, s):
+            self.cuda_stream = s.cuda_stream
+
+    pc, s = make(), torch.cuda.Stream()
+    want = lens(wants[0])
+    torch.cuda.synchronize()
+    got = step(pc, want, xs[0], stream=Handle(s))
+    pc.check(stream=Handle(s))
+    assert torch.equal(got[:total[0]], outs[0])
+
+
+def test_built_inside_a_capture():
+    """Its tensors are set by the replay."""
+    q, k, v = inputs(4)
+    want = lens([10, 0, 3])
+    step(make(), want, (q, k, v))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pc = make()
+        got = step(pc, want, (q, k, v))
+    for _ in range(2):
+        graph.replay()
+        pc.check()
+        assert pc.lens.tolist() == [10, 0, 3]
+        assert torch.equal(got[:13], step(make(), want, (q, k, v))[:13])

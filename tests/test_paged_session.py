@@ -26,7 +26,8 @@ def calls(monkeypatch):
         inside.pop()
 
     monkeypatch.setattr(torch.cuda, "device", device)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream("current", d or inside[-1]))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: inside[-1].index)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0x100 + index, raising=False)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda d=None: Stream("default", d))
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device: Stream(h, device))
     for name in ("resize", "kv_write", "attention"):
@@ -54,7 +55,7 @@ def test_calls_switch_to_the_cache_s_device_and_its_current_stream(calls):
     step(pc)
     assert [name for name, _, _ in seen] == ["resize", "kv_write", "attention", "check"]
     for _, dev, stream in seen:
-        assert dev == pc.device and stream.name == "current" and stream.device == pc.device
+        assert dev == pc.device and stream == 0x101
 
 
 def test_streams_given(calls):
